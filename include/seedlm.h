@@ -80,8 +80,9 @@ typedef struct seedlm_format {
                       /* (8,3): ignored                                           */
 } seedlm_format;
 
-/* Activation element types. */
-enum { SEEDLM_F16 = 0, SEEDLM_BF16 = 1 };
+/* Element types: activations are SEEDLM_F16 or SEEDLM_BF16; the residual
+ * stream and the parameters of seedlm_block_norm may also be SEEDLM_F32. */
+enum { SEEDLM_F16 = 0, SEEDLM_BF16 = 1, SEEDLM_F32 = 2 };
 
 /* Error codes. */
 enum {
@@ -264,6 +265,123 @@ SEEDLM_API int seedlm_search_blocks(int32_t C, int32_t P, int32_t K, const float
  * 2^K - 1 nonzero states.  0 for K outside 8..20.  HOST function. */
 SEEDLM_API uint32_t seedlm_lfsr_taps(int32_t K);
 
+/* ---- What runs between the products of a decoder layer (no counterpart in
+ * the pages: the method compresses the products' weights and leaves these as
+ * they are).  They take and give the products' own types -- fp32 sums out of
+ * a product, fp16 or bf16 activations into one -- and follow the conventions
+ * above; leading dimensions and strides count elements.  Every kernel waits
+ * for the work before it on the stream before it reads or writes memory, so
+ * calls chain with the products without synchronisation.
+ *
+ * Low-rank adapters beside a shared projection.  The projection's outputs
+ * are cut into `slices` parts (q, k, v of a fused projection; gate and up),
+ * part s with rows[s] outputs and adapter matrices of its own:
+ *     Y[m][part s] = base[m][part s] + scale_a * (x_m A_{s,a}^T) B_{s,a}^T
+ * where a is the adapter of row m.  A_{s,a} is rank x cols at
+ * A[s] + a * a_adapter[s], row r at + r * a_row[s]; B_{s,a} is rows[s] x rank
+ * at B[s] + a * b_adapter[s], row j at + j * b_row[s].  Adapter a uses the
+ * first ranks[a] rows of A and columns of B (clamped to 0..rank; what lies
+ * beyond is never read); ranks == NULL: all use `rank`.  scales == NULL: 1. */
+enum { SEEDLM_MAX_SLICES = 4, SEEDLM_MAX_RANK = 256, SEEDLM_MAX_ADAPTERS = 1024 };
+
+typedef struct seedlm_adapters {
+  int32_t n;          /* adapters, 1..SEEDLM_MAX_ADAPTERS                        */
+  int32_t rank;       /* largest rank, 1..SEEDLM_MAX_RANK                        */
+  int32_t cols;       /* inputs of the projection, >= 0                          */
+  int32_t slices;     /* 1..SEEDLM_MAX_SLICES                                    */
+  int32_t dtype;      /* of A and B, and of X: SEEDLM_F16 or SEEDLM_BF16         */
+  int32_t rows[4];    /* outputs of each slice, >= 0 (their sum below 2^31)      */
+  const void* A[4];
+  const void* B[4];
+  int64_t a_adapter[4], a_row[4], b_adapter[4], b_row[4];  /* >= 0               */
+  const int32_t* ranks;   /* DEVICE, n entries, or NULL                          */
+  const float* scales;    /* DEVICE, n entries, or NULL                          */
+} seedlm_adapters;
+
+/* The rows of a batch sorted by adapter, made once for a batch and used by
+ * seedlm_adapters_apply for every projection it passes.  M: 0 to 2^24 rows
+ * (more: SEEDLM_EUNSUPPORTED, there as here).  ids: M int32, the
+ * adapter of each row; any value outside 0..n-1 means none.  plan: device
+ * memory of seedlm_adapters_plan_words(M, n) int32, 16-byte aligned.
+ * plan[0, M) receives the row numbers in the order of their adapter, those of
+ * one adapter in increasing order, those without an adapter last;
+ * plan[M, M + n + 1) receives the offsets: the rows of adapter a are
+ * plan[plan[M + a]] .. plan[plan[M + a + 1] - 1], those without one start at
+ * plan[M + n].  The rest of the plan is the library's. */
+SEEDLM_API int seedlm_adapters_plan(int32_t M, int32_t n, const int32_t* ids, int32_t* plan,
+                                    seedlm_stream stream);
+
+/* int32 words a plan takes (HOST function; negative on a bad argument). */
+SEEDLM_API int64_t seedlm_adapters_plan_words(int32_t M, int32_t n);
+
+/* Adds the adapters of a batch to its projection (see above).  X: M x cols
+ * of type ad->dtype, leading dimension ldx; base and Y: M x sum(rows) fp32,
+ * leading dimensions ldb and ldy.  base == NULL or base == Y (then with
+ * ldb == ldy) adds in place, and rows without an adapter are neither read
+ * nor written; a base that overlaps Y in another way gives undefined
+ * results.  plan: made by seedlm_adapters_plan for this M and ad->n; a plan
+ * made for others changes nothing in Y and sets value 4 of
+ * seedlm_device_error.  Sums are fp32 in a fixed order per shape; x A^T is
+ * kept to 24 bits between the two products.  Any alignment of X, A, B, base
+ * and Y that their types allow is accepted; 16-byte aligned arrays with
+ * strides and row counts that keep every row aligned are read 16 bytes at a
+ * time.  `workspace`: device memory of at least
+ * seedlm_adapters_workspace_bytes(ad, M) bytes, 256-byte aligned, of any
+ * content; calls that share one must not run concurrently (calls on one
+ * stream never do). */
+SEEDLM_API int seedlm_adapters_apply(const seedlm_adapters* ad, const int32_t* plan, int32_t M,
+                                     const void* X, int64_t ldx, const float* base, int64_t ldb,
+                                     float* Y, int64_t ldy, void* workspace,
+                                     int64_t workspace_bytes, seedlm_stream stream);
+
+/* Workspace bytes seedlm_adapters_apply needs on the current device (HOST
+ * function; negative on error). */
+SEEDLM_API int64_t seedlm_adapters_workspace_bytes(const seedlm_adapters* ad, int32_t M);
+
+/* The end of one block and the start of the next, per row of a batch:
+ *     v  = norm_post(y) if nm->post, else y        (y: a product's fp32 sums)
+ *     h' = h_scale * h + y_scale * gate * v        (the residual stream)
+ *     x  = norm_pre(h') if nm->pre, else h'        (the next product's input)
+ *   RMS:   norm(v) = v / sqrt(mean(v^2) + eps) * (weight_offset + w) + b
+ *   LAYER: norm(v) = (v - mean(v)) / sqrt(var(v) + eps) * (weight_offset + w) + b
+ * Computed in fp32; h' and x are each rounded once, and norm_pre takes h'
+ * before its rounding. */
+enum { SEEDLM_NORM_RMS = 0, SEEDLM_NORM_LAYER = 1 };
+
+typedef struct seedlm_norm {
+  int32_t cols;           /* width of a row, 0..SEEDLM_MAX_NORM_COLS               */
+  int32_t kind;           /* SEEDLM_NORM_RMS or SEEDLM_NORM_LAYER                  */
+  int32_t dtype;          /* of weights, biases and gate: F16, BF16 or F32         */
+  int32_t post, pre;      /* 0 or 1: whether each of the two norms is applied      */
+  float eps;              /* >= 0                                                  */
+  float weight_offset;    /* added to every weight (1 where 1 + w is stored as w)  */
+  float h_scale, y_scale;
+  const void *w_post, *b_post, *w_pre, *b_pre;  /* cols entries each, or NULL:     */
+                          /* weight_offset + w is then 1, b is 0                   */
+} seedlm_norm;
+enum { SEEDLM_MAX_NORM_COLS = 1 << 20 };
+
+/* y: M x cols fp32 or NULL (taken as 0; the gate is then not read); h: M x
+ * cols of h_dtype (F16, BF16 or F32) or NULL (taken as 0), not both NULL;
+ * gate: type nm->dtype, one row for all (ldg == 0) or one for each row of
+ * the batch (ldg >= cols), or NULL (1).  h_out (type h_dtype; h_out == h with
+ * ldho == ldh updates in place) and x (SEEDLM_F16 or SEEDLM_BF16) may each be
+ * NULL, not both.  Other overlaps of outputs with inputs give undefined
+ * results. */
+SEEDLM_API int seedlm_block_norm(const seedlm_norm* nm, int32_t M, const float* y, int64_t ldy,
+                                 const void* gate, int64_t ldg, const void* h, int64_t ldh,
+                                 void* h_out, int64_t ldho, int h_dtype, void* x, int64_t ldx,
+                                 int x_dtype, seedlm_stream stream);
+
+/* The gated activation between a fused gate+up product and the down product:
+ * X[m][f] = act(GU[m][f]) * GU[m][cols + f], GU M x 2 cols fp32, X M x cols
+ * SEEDLM_F16 or SEEDLM_BF16, computed in fp32 and rounded once.
+ *   SILU: g / (1 + e^-g)   GELU: g/2 (1 + erf(g / sqrt 2))
+ *   GELU_TANH: g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+enum { SEEDLM_SILU = 0, SEEDLM_GELU = 1, SEEDLM_GELU_TANH = 2 };
+SEEDLM_API int seedlm_glu(int32_t M, int32_t cols, int act, const float* GU, int64_t ldgu, void* X,
+                          int64_t ldx, int x_dtype, seedlm_stream stream);
+
 /* Failure-path self test (no counterpart in the pages): launches one small
  * kernel whose bounded mbarrier wait -- the wait the tensor-core GEMM uses,
  * with its TMEM allocation -- waits for an arrival that never comes and gives
@@ -277,7 +395,9 @@ SEEDLM_API int seedlm_selftest_wait_timeout(int64_t limit_ns, seedlm_stream stre
  * barriers, bit 1 (value 2) if a kernel of a checked build (below) computed a
  * memory index outside the buffers its arguments describe, or a
  * shared-memory index outside its launch's allocation, and skipped that
- * access.  The outputs of such a call are undefined.  0 if neither happened.
+ * access, bit 2 (value 4) if seedlm_adapters_apply was given a plan made for
+ * another batch size or number of adapters and changed nothing.  The outputs
+ * of such a call are undefined.  0 if nothing happened.
  * HOST function; synchronous. */
 SEEDLM_API int seedlm_device_error(int* flag);
 

@@ -114,6 +114,31 @@ int64_t gemm_any_workspace(const seedlm_format& f, int M, const DeviceInfo& dev)
   return need;
 }
 
+bool act_dtype(int t) { return t == SEEDLM_F16 || t == SEEDLM_BF16; }
+bool any_dtype(int t) { return act_dtype(t) || t == SEEDLM_F32; }
+uintptr_t bytes_of(int t) { return t == SEEDLM_F32 ? 4 : 2; }
+
+// The adapters' description alone; *total receives the sum of the slices' rows.
+int check_adapters(const seedlm_adapters* ad, int64_t* total) {
+  if (!ad || ad->n < 1 || ad->rank < 1 || ad->cols < 0 || ad->slices < 1) return SEEDLM_EINVAL;
+  if (ad->n > SEEDLM_MAX_ADAPTERS || ad->rank > SEEDLM_MAX_RANK) return SEEDLM_EUNSUPPORTED;
+  if (ad->slices > SEEDLM_MAX_SLICES) return SEEDLM_EUNSUPPORTED;
+  if (!act_dtype(ad->dtype)) return SEEDLM_EINVAL;
+  *total = 0;
+  for (int s = 0; s < ad->slices; ++s) {
+    if (ad->rows[s] < 0 || ad->a_adapter[s] < 0 || ad->a_row[s] < 0 || ad->b_adapter[s] < 0 ||
+        ad->b_row[s] < 0)
+      return SEEDLM_EINVAL;
+    if (ad->rows[s] > 0 && ad->cols > 0 && (!ad->A[s] || !aligned(ad->A[s], 2))) return SEEDLM_EINVAL;
+    if (ad->rows[s] > 0 && (!ad->B[s] || !aligned(ad->B[s], 2))) return SEEDLM_EINVAL;
+    *total += ad->rows[s];
+  }
+  if (*total > INT32_MAX) return SEEDLM_EINVAL;
+  if ((ad->ranks && !aligned(ad->ranks, 4)) || (ad->scales && !aligned(ad->scales, 4)))
+    return SEEDLM_EINVAL;
+  return SEEDLM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -289,6 +314,100 @@ int seedlm_encode(const seedlm_format* fmt, const float* W, int64_t ldw, uint32_
   return launch_encode(*fmt, W, ldw, rec, eplane, err, (cudaStream_t)stream, dev);
 }
 
+int64_t seedlm_adapters_plan_words(int32_t M, int32_t n) {
+  if (M < 0 || M > kMaxAdapterRows || n < 1 || n > SEEDLM_MAX_ADAPTERS) return SEEDLM_EINVAL;
+  return adapters_plan_words(M, n);
+}
+
+int seedlm_adapters_plan(int32_t M, int32_t n, const int32_t* ids, int32_t* plan,
+                         seedlm_stream stream) {
+  if (M < 0 || n < 1) return SEEDLM_EINVAL;
+  if (M > kMaxAdapterRows || n > SEEDLM_MAX_ADAPTERS) return SEEDLM_EUNSUPPORTED;
+  if (!plan || !aligned(plan, 16) || (M > 0 && (!ids || !aligned(ids, 4)))) return SEEDLM_EINVAL;
+  DeviceInfo dev;
+  int rc = device_info(&dev);
+  if (rc) return rc;
+  return launch_adapters_plan(M, n, ids, plan, (cudaStream_t)stream, dev);
+}
+
+int64_t seedlm_adapters_workspace_bytes(const seedlm_adapters* ad, int32_t M) {
+  int64_t total;
+  if (check_adapters(ad, &total) || M < 0 || M > kMaxAdapterRows) return SEEDLM_EINVAL;
+  if (M == 0 || total == 0) return 0;
+  DeviceInfo dev;
+  int rc = device_info(&dev);
+  if (rc) return rc;
+  return adapters_workspace_bytes(*ad, M, dev);
+}
+
+int seedlm_adapters_apply(const seedlm_adapters* ad, const int32_t* plan, int32_t M, const void* X,
+                          int64_t ldx, const float* base, int64_t ldb, float* Y, int64_t ldy,
+                          void* workspace, int64_t workspace_bytes, seedlm_stream stream) {
+  int64_t total;
+  int rc = check_adapters(ad, &total);
+  if (rc) return rc;
+  if (M < 0 || workspace_bytes < 0) return SEEDLM_EINVAL;
+  if (M > kMaxAdapterRows) return SEEDLM_EUNSUPPORTED;
+  if (M == 0 || total == 0) return SEEDLM_OK;
+  if (!plan || !aligned(plan, 16)) return SEEDLM_EINVAL;
+  if (ad->cols > 0 && (!X || !aligned(X, 2) || ldx < ad->cols)) return SEEDLM_EINVAL;
+  if (!Y || !aligned(Y, 4) || ldy < total) return SEEDLM_EINVAL;
+  if (!base) {
+    base = Y;
+    ldb = ldy;
+  }
+  if (!aligned(base, 4) || ldb < total || (base == Y && ldb != ldy)) return SEEDLM_EINVAL;
+  DeviceInfo dev;
+  if ((rc = device_info(&dev))) return rc;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < adapters_workspace_bytes(*ad, M, dev))
+    return SEEDLM_EINVAL;
+  return launch_adapters_apply(*ad, plan, M, static_cast<const uint16_t*>(X), ldx, base, ldb, Y, ldy,
+                               workspace, (cudaStream_t)stream, dev);
+}
+
+int seedlm_block_norm(const seedlm_norm* nm, int32_t M, const float* y, int64_t ldy,
+                      const void* gate, int64_t ldg, const void* h, int64_t ldh, void* h_out,
+                      int64_t ldho, int h_dtype, void* x, int64_t ldx, int x_dtype,
+                      seedlm_stream stream) {
+  if (!nm || M < 0 || nm->cols < 0) return SEEDLM_EINVAL;
+  if (nm->cols > SEEDLM_MAX_NORM_COLS) return SEEDLM_EUNSUPPORTED;
+  if (nm->kind != SEEDLM_NORM_RMS && nm->kind != SEEDLM_NORM_LAYER) return SEEDLM_EINVAL;
+  if (!any_dtype(nm->dtype) || (nm->post | 1) != 1 || (nm->pre | 1) != 1) return SEEDLM_EINVAL;
+  if (!(nm->eps >= 0.f)) return SEEDLM_EINVAL;
+  if ((!y && !h) || (!h_out && !x)) return SEEDLM_EINVAL;
+  if ((h || h_out) && !any_dtype(h_dtype)) return SEEDLM_EINVAL;
+  if (x && !act_dtype(x_dtype)) return SEEDLM_EINVAL;
+  const uintptr_t pb = bytes_of(nm->dtype), hb = bytes_of(h_dtype);
+  for (const void* w : {nm->w_post, nm->b_post, nm->w_pre, nm->b_pre})
+    if (w && !aligned(w, pb)) return SEEDLM_EINVAL;
+  if (y && (!aligned(y, 4) || ldy < nm->cols)) return SEEDLM_EINVAL;
+  if (gate && (!aligned(gate, pb) || (ldg != 0 && ldg < nm->cols))) return SEEDLM_EINVAL;
+  if (h && (!aligned(h, hb) || ldh < nm->cols)) return SEEDLM_EINVAL;
+  if (h_out && (!aligned(h_out, hb) || ldho < nm->cols)) return SEEDLM_EINVAL;
+  if (h && h == h_out && ldh != ldho) return SEEDLM_EINVAL;
+  if (x && (!aligned(x, 2) || ldx < nm->cols)) return SEEDLM_EINVAL;
+  if (M == 0 || nm->cols == 0) return SEEDLM_OK;
+  DeviceInfo dev;
+  int rc = device_info(&dev);
+  if (rc) return rc;
+  return launch_block_norm(*nm, M, y, ldy, gate, ldg, h, ldh, h_out, ldho, h_dtype, x, ldx, x_dtype,
+                           (cudaStream_t)stream, dev);
+}
+
+int seedlm_glu(int32_t M, int32_t cols, int act, const float* GU, int64_t ldgu, void* X,
+               int64_t ldx, int x_dtype, seedlm_stream stream) {
+  if (M < 0 || cols < 0 || act < SEEDLM_SILU || act > SEEDLM_GELU_TANH) return SEEDLM_EINVAL;
+  if (!act_dtype(x_dtype)) return SEEDLM_EINVAL;
+  if (M == 0 || cols == 0) return SEEDLM_OK;
+  if (!GU || !aligned(GU, 4) || ldgu < 2 * (int64_t)cols) return SEEDLM_EINVAL;
+  if (!X || !aligned(X, 2) || ldx < cols) return SEEDLM_EINVAL;
+  DeviceInfo dev;
+  int rc = device_info(&dev);
+  if (rc) return rc;
+  return launch_glu(M, cols, act, GU, ldgu, X, ldx, x_dtype, (cudaStream_t)stream, dev);
+}
+
 int seedlm_selftest_wait_timeout(int64_t limit_ns, seedlm_stream stream) {
   if (limit_ns < 1000 || limit_ns > 100000000) return SEEDLM_EINVAL;
   DeviceInfo dev;
@@ -325,12 +444,15 @@ int seedlm_device_error(int* flag) {
   int (*const readers[])(unsigned int*) = {read_and_clear_check_gemv, read_and_clear_check_decompress,
                                            read_and_clear_check_gemm_tc, read_and_clear_check_encode,
                                            read_and_clear_check_dense, read_and_clear_check_gemm_cc,
-                                           read_and_clear_check_gemv_amort};
+                                           read_and_clear_check_gemv_amort, read_and_clear_check_adapters,
+                                           read_and_clear_check_block_norm};
   for (auto read : readers) {
     unsigned int c = 0;
     if ((rc = read(&c))) return rc;
     if (c) out |= 2;
   }
+  if ((rc = read_and_clear_plan_mismatch(&v))) return rc;
+  if (v) out |= 4;
   *flag = out;
   return SEEDLM_OK;
 }

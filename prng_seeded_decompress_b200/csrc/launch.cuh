@@ -1,0 +1,45 @@
+// launch.cuh -- launching kernels with programmatic dependent launch: the
+// kernel may start while the one before it on the stream is finishing, and
+// calls grid_wait() before it reads or writes anything that kernel touches.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <utility>
+
+#include "seedlm_internal.h"
+
+namespace seedlm {
+
+// Returns once every grid before this one on the stream has completed and
+// its writes are visible.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Lets the next grid on the stream start once every CTA of this one has called
+// this or ended.
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <class... Params, class... Args>
+int launch_pdl(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+  if (err != cudaSuccess) {
+    cudaGetLastError();  // the caller has the error; the next call starts clean
+    return record_cuda_error(err);
+  }
+  count_launch();
+  return SEEDLM_OK;
+}
+
+}  // namespace seedlm

@@ -17,6 +17,10 @@ LIB_PATH = os.path.join(PKG, "libseedlm_check.so" if CHECKED else "libseedlm.so"
 
 F16 = 0
 BF16 = 1
+F32 = 2
+
+#: Largest numbers of slices, rank and adapters of one Adapters (include/seedlm.h).
+MAX_SLICES, MAX_RANK, MAX_ADAPTERS = 4, 256, 1024
 
 #: Every symbol include/seedlm.h declares.
 EXPORTS = (
@@ -27,7 +31,8 @@ EXPORTS = (
     "seedlm_strerror", "seedlm_last_cuda_error", "seedlm_launch_count", "seedlm_shutdown",
     "seedlm_encode", "seedlm_selftest_wait_timeout", "seedlm_checked_build",
     "seedlm_selftest_bounds_check", "seedlm_search_blocks", "seedlm_lfsr_taps",
-    "seedlm_gemv_batch",
+    "seedlm_gemv_batch", "seedlm_adapters_plan", "seedlm_adapters_plan_words",
+    "seedlm_adapters_apply", "seedlm_adapters_workspace_bytes", "seedlm_block_norm", "seedlm_glu",
 )
 
 
@@ -45,6 +50,19 @@ class Format(ctypes.Structure):
     def from_dict(cls, d: dict) -> "Format":
         return cls(*(int(d[k]) for k in ("C", "P", "K", "rows", "cols", "nb", "rec_pitch",
                                          "e_pitch")))
+
+
+class _AdaptersStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n", "rank", "cols", "slices", "dtype")] + \
+        [("rows", ctypes.c_int32 * 4), ("A", ctypes.c_void_p * 4), ("B", ctypes.c_void_p * 4)] + \
+        [(n, ctypes.c_int64 * 4) for n in ("a_adapter", "a_row", "b_adapter", "b_row")] + \
+        [("ranks", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class _NormStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("cols", "kind", "dtype", "post", "pre")] + \
+        [(n, ctypes.c_float) for n in ("eps", "weight_offset", "h_scale", "y_scale")] + \
+        [(n, ctypes.c_void_p) for n in ("w_post", "b_post", "w_pre", "b_pre")]
 
 
 def _load():
@@ -81,6 +99,14 @@ def _load():
         "seedlm_search_blocks": (ctypes.c_int, [i32, i32, i32, vp, i64, vp, vp, vp, vp, vp]),
         "seedlm_lfsr_taps": (ctypes.c_uint32, [i32]),
         "seedlm_gemv_batch": (ctypes.c_int, [i32, vp, vp, vp, vp, ctypes.c_int, vp, vp]),
+        "seedlm_adapters_plan": (ctypes.c_int, [i32, i32, vp, vp, vp]),
+        "seedlm_adapters_plan_words": (i64, [i32, i32]),
+        "seedlm_adapters_apply": (ctypes.c_int, [vp, vp, i32, vp, i64, vp, i64, vp, i64, vp, i64,
+                                                 vp]),
+        "seedlm_adapters_workspace_bytes": (i64, [vp, i32]),
+        "seedlm_block_norm": (ctypes.c_int, [vp, i32, vp, i64, vp, i64, vp, i64, vp, i64,
+                                             ctypes.c_int, vp, i64, ctypes.c_int, vp]),
+        "seedlm_glu": (ctypes.c_int, [i32, i32, ctypes.c_int, vp, i64, vp, i64, ctypes.c_int, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -337,3 +363,258 @@ def row_bytes(fmt) -> tuple[int, int]:
     f = _fmt(fmt)
     return int(lib.seedlm_row_bytes_ideal(ctypes.byref(f))), \
         int(lib.seedlm_row_bytes_stored(ctypes.byref(f)))
+
+
+# ---------------------------------------------- what runs between the products
+
+def _any_dtype(t) -> int:
+    import torch
+    return F32 if t.dtype == torch.float32 else _act_dtype(t)
+
+
+def _rows_ld(t, M: int, cols: int, name: str) -> int:
+    """Leading dimension of an M x cols argument with unit column stride."""
+    if t.dim() != 2 or t.shape[0] != M or t.shape[1] != cols:
+        raise ValueError(f"{name} must be {M} x {cols}, got {tuple(t.shape)}")
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return ld if M > 1 else max(ld, cols)
+
+
+def _is_f32(t, name: str):
+    import torch
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32, got {t.dtype}")
+    return t
+
+
+def _run_on(device: int, tensors, stream, fn: str, call):
+    """call(stream) with `device` current; every tensor must live there."""
+    import torch
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("every tensor of a call must be on the same CUDA device")
+    if device < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if device == torch.cuda.current_device():
+        _check(fn, call(stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn, call(stream))
+
+
+class Adapters:
+    """Low-rank adapters of one projection.
+
+    A: (n, rank, cols), B: (n, rows, rank), float16 or bfloat16, unit stride in
+    the last dimension -- or lists of 1 to 4 such tensors, one pair for each
+    part of a fused projection (q, k, v; gate, up), whose outputs lie side by
+    side.  ranks: int32 (n), how much of A and B each adapter uses (all of it if
+    None).  scales: float32 (n), or None for 1.  The tensors are kept, not
+    copied: what is written into them later is what later calls use."""
+
+    def __init__(self, A, B, ranks=None, scales=None):
+        import torch
+        A = list(A) if isinstance(A, (list, tuple)) else [A]
+        B = list(B) if isinstance(B, (list, tuple)) else [B]
+        if not 1 <= len(A) <= MAX_SLICES or len(A) != len(B):
+            raise ValueError(f"one B for each A, 1 to {MAX_SLICES} of them")
+        for a, b in zip(A, B):
+            if a.dim() != 3 or b.dim() != 3:
+                raise ValueError("A must be (n, rank, cols) and B (n, rows, rank)")
+            if a.shape != A[0].shape or b.shape[0] != a.shape[0] or b.shape[2] != a.shape[1]:
+                raise ValueError("every A must have one shape, and B (n, rows, rank) its n and rank")
+            if a.dtype != A[0].dtype or b.dtype != A[0].dtype:
+                raise TypeError("A and B must have one element type")
+            if (a.shape[2] > 1 and a.stride(2) != 1) or (b.shape[2] > 1 and b.stride(2) != 1):
+                raise ValueError("A and B must have unit stride in their last dimension")
+        n, rank, cols = (int(v) for v in A[0].shape)
+        for t, name, dt in ((ranks, "ranks", torch.int32), (scales, "scales", torch.float32)):
+            if t is None:
+                continue
+            if t.dtype != dt:
+                raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+            if t.dim() != 1 or t.shape[0] != n:
+                raise ValueError(f"{name} must have {n} entries")
+            _dense(t, name)
+        self.n, self.rank, self.cols, self.dtype = n, rank, cols, A[0].dtype
+        self.rows = [int(b.shape[1]) for b in B]
+        self.total_rows = sum(self.rows)
+        self.tensors = [*A, *B, ranks, scales]
+        self.device = A[0].get_device()
+        s = _AdaptersStruct(n, rank, cols, len(A), _act_dtype(A[0]))
+        for i, (a, b) in enumerate(zip(A, B)):
+            s.rows[i], s.A[i], s.B[i] = b.shape[1], a.data_ptr(), b.data_ptr()
+            s.a_adapter[i], s.a_row[i] = a.stride(0), a.stride(1)
+            s.b_adapter[i], s.b_row[i] = b.stride(0), b.stride(1)
+        s.ranks, s.scales = _ptr(ranks), _ptr(scales)
+        self.struct = s
+        self.ref = ctypes.byref(s)
+
+
+class AdapterPlan:
+    """Room for the plan of a batch of M rows and n adapters.  After
+    adapter_plan(): order (int32, M) holds the rows in the order of their
+    adapter, those without one last; the rows of adapter a are
+    order[offsets[a]:offsets[a + 1]], offsets int32 (n + 1)."""
+
+    def __init__(self, M: int, n: int, device=None):
+        import torch
+        words = int(lib.seedlm_adapters_plan_words(int(M), int(n)))
+        if words < 0:
+            _check("seedlm_adapters_plan_words", words)
+        self.M, self.n = int(M), int(n)
+        self.buffer = torch.zeros(words, dtype=torch.int32, device=device or "cuda")
+        self.order = self.buffer[:self.M]
+        self.offsets = self.buffer[self.M:self.M + self.n + 1]
+
+
+def adapter_plan(ids, n: int, plan: AdapterPlan | None = None, stream=None) -> AdapterPlan:
+    """Sort a batch's rows by adapter: ids int32 (M), a value outside 0..n-1
+    for a row without one.  The result serves every adapter_apply() of the
+    batch; `plan` (for M rows and n adapters) is written again if given."""
+    import torch
+    if ids.dtype != torch.int32 or ids.dim() != 1:
+        raise TypeError("ids must be a vector of int32")
+    _dense(ids, "ids")
+    M = ids.shape[0]
+    if plan is None:
+        plan = AdapterPlan(M, n, device=ids.device)
+    elif plan.M != M or plan.n != n:
+        raise ValueError(f"the plan is for {plan.M} rows and {plan.n} adapters, not {M} and {n}")
+    _run_on(ids.get_device(), (plan.buffer,), stream, "seedlm_adapters_plan",
+            lambda st: lib.seedlm_adapters_plan(M, plan.n, ids.data_ptr(), plan.buffer.data_ptr(),
+                                                st))
+    return plan
+
+
+def adapter_workspace_bytes(adapters: Adapters, M: int) -> int:
+    n = int(lib.seedlm_adapters_workspace_bytes(adapters.ref, int(M)))
+    if n < 0:
+        _check("seedlm_adapters_workspace_bytes", n)
+    return n
+
+
+def adapter_workspace(adapters: Adapters, M: int):
+    """A device workspace for adapter_apply() on M rows.  It serves every later
+    call with the same or a smaller need; calls that share it must not run
+    concurrently."""
+    import torch
+    with torch.cuda.device(adapters.device):
+        n = adapter_workspace_bytes(adapters, M)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=f"cuda:{adapters.device}")
+
+
+def adapter_apply(adapters: Adapters, plan: AdapterPlan, X, Y, base=None, workspace=None,
+                  stream=None):
+    """Y = base + scale_a (X A_a^T) B_a^T, row by row with the row's adapter a;
+    base None adds to Y in place.  X (M, cols) of the adapters' type; Y and
+    base float32 (M, total rows).  `workspace` comes from adapter_workspace();
+    if omitted a fresh one is made."""
+    M = plan.M
+    if X.dtype != adapters.dtype:
+        raise TypeError(f"X must be {adapters.dtype} as the adapters are, got {X.dtype}")
+    if plan.n != adapters.n:
+        raise ValueError(f"the plan is for {plan.n} adapters, not {adapters.n}")
+    ldx = _rows_ld(X, M, adapters.cols, "X")
+    ldy = _rows_ld(_is_f32(Y, "Y"), M, adapters.total_rows, "Y")
+    ldb = ldy if base is None else _rows_ld(_is_f32(base, "base"), M, adapters.total_rows, "base")
+    if workspace is None:
+        workspace = adapter_workspace(adapters, M)
+    _run_on(adapters.device, (X, Y, base, plan.buffer, workspace, *adapters.tensors), stream,
+            "seedlm_adapters_apply",
+            lambda st: lib.seedlm_adapters_apply(
+                adapters.ref, plan.buffer.data_ptr(), M, X.data_ptr(), ldx, _ptr(base), ldb,
+                Y.data_ptr(), ldy, workspace.data_ptr(),
+                workspace.numel() * workspace.element_size(), st))
+
+
+class BlockNorm:
+    """The parameters of block_norm(): norms of kind "rms" or "layer" with
+    weights (weight_offset is added to them) and biases of one type (float16,
+    bfloat16 or float32; None for 1 and 0), and the scales of the sum.  A norm
+    after the block is applied if post is true (by default: if w_post or b_post
+    is given), one before the next unless pre is false."""
+
+    def __init__(self, cols: int, kind: str = "rms", eps: float = 1e-6, h_scale: float = 1.0,
+                 y_scale: float = 1.0, weight_offset: float = 0.0, w_post=None, b_post=None,
+                 w_pre=None, b_pre=None, post: bool | None = None, pre: bool = True, dtype=None):
+        import torch
+        if kind not in ("rms", "layer"):
+            raise ValueError(f"kind must be 'rms' or 'layer', got {kind!r}")
+        given = [t for t in (w_post, b_post, w_pre, b_pre) if t is not None]
+        self.dtype = dtype or (given[0].dtype if given else torch.float32)
+        for t in given:
+            if t.dtype != self.dtype:
+                raise TypeError("weights and biases must have one element type")
+            if t.dim() != 1 or t.shape[0] != cols:
+                raise ValueError(f"weights and biases must have {cols} entries")
+            _dense(t, "a weight or bias")
+        self.cols = int(cols)
+        self.tensors = given
+        post = w_post is not None or b_post is not None if post is None else bool(post)
+        self.struct = _NormStruct(
+            self.cols, 1 if kind == "layer" else 0, _any_dtype(torch.empty(0, dtype=self.dtype)),
+            int(post), int(bool(pre)), eps, weight_offset, h_scale, y_scale,
+            _ptr(w_post), _ptr(b_post), _ptr(w_pre), _ptr(b_pre))
+        self.ref = ctypes.byref(self.struct)
+
+
+def block_norm(norm: BlockNorm, y, h, h_out=None, x=None, gate=None, stream=None):
+    """v = norm_post(y); h_out = h_scale h + y_scale gate v; x = norm_pre(h_out)
+    before its rounding.  y float32 (M, cols) or None for 0; h and h_out of
+    one type (float16, bfloat16 or float32), h None for 0, h_out may be h; x
+    float16/bfloat16; h_out or x may be None.  gate: (cols) or (M, cols) of the
+    norm's type, or None for 1."""
+    like = y if y is not None else h
+    if like is None or (h_out is None and x is None):
+        raise ValueError("y or h, and h_out or x, must be given")
+    M, cols = like.shape[0] if like.dim() else 0, norm.cols
+    ldy = ldg = ldh = ldo = ldx = 0
+    if y is not None:
+        ldy = _rows_ld(_is_f32(y, "y"), M, cols, "y")
+    ht = xt = 0
+    if h is not None:
+        ldh, ht = _rows_ld(h, M, cols, "h"), _any_dtype(h)
+    if h_out is not None:
+        ldo, ht = _rows_ld(h_out, M, cols, "h_out"), _any_dtype(h_out)
+        if h is not None and h.dtype != h_out.dtype:
+            raise TypeError("h and h_out must have one element type")
+    if x is not None:
+        ldx, xt = _rows_ld(x, M, cols, "x"), _act_dtype(x)
+    if gate is not None:
+        if gate.dtype != norm.dtype:
+            raise TypeError(f"gate must be {norm.dtype} as the norm's parameters are")
+        if gate.dim() == 1:
+            if gate.shape[0] != cols:
+                raise ValueError(f"gate must have {cols} or {M} x {cols} entries")
+            _dense(gate, "gate")
+        else:
+            ldg = _rows_ld(gate, M, cols, "gate")
+    _run_on(like.get_device(), (y, h, h_out, x, gate, *norm.tensors), stream, "seedlm_block_norm",
+            lambda st: lib.seedlm_block_norm(norm.ref, M, _ptr(y), ldy, _ptr(gate), ldg, _ptr(h),
+                                             ldh, _ptr(h_out), ldo, ht, _ptr(x), ldx, xt, st))
+
+
+#: Activations of glu().
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def glu(GU, X, act: str = "silu", stream=None):
+    """X = act(GU[:, :cols]) * GU[:, cols:]; GU float32 (M, 2 cols), X
+    float16/bfloat16 (M, cols); act "silu", "gelu" or "gelu_tanh"."""
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+    if X.dim() != 2:
+        raise ValueError("X must be M x cols")
+    M, cols = X.shape
+    ldx, xt = _rows_ld(X, M, cols, "X"), _act_dtype(X)
+    ldgu = _rows_ld(_is_f32(GU, "GU"), M, 2 * cols, "GU")
+    _run_on(X.get_device(), (GU,), stream, "seedlm_glu",
+            lambda st: lib.seedlm_glu(M, cols, ACTIVATIONS[act], GU.data_ptr(), ldgu, X.data_ptr(),
+                                      ldx, xt, st))
