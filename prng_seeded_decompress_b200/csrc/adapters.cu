@@ -152,20 +152,30 @@ adapters_plan_kernel(int M, int n, int T, const int32_t* __restrict__ ids, int32
 // ------------------------------------------------------------- the products
 //
 // Two kernels.  The first takes the sums S = s_a x A_a^T, the second adds
-// S B_a^T to the outputs.  Both feed mma.sync with fragments loaded straight
-// from memory: of a contraction step of 32, the lane in column q of its quad
+// S B_a^T to the outputs.  Both feed mma.sync with fragments that need no
+// shuffling: of a contraction step of 32, the lane in column q of its quad
 // takes elements 8q .. 8q + 7 with one 16-byte load and gives words 0, 1 to a
 // first m16n8k16 product and words 2, 3 to a second.  The order of the
-// contraction does not matter as long as both operands are read alike, so no
-// operand is staged or shuffled.  The matrix of adapter weights is the
-// operand of 16 rows and the tile's activations the one of 8 columns, so a
-// request that is alone with its adapter wastes tensor work, which is idle
-// here, and no memory traffic, which is what bounds both kernels.
+// contraction does not matter as long as both operands are read alike.  The
+// matrix of adapter weights is the operand of 16 rows and the tile's
+// activations the one of 8 columns, so a request that is alone with its
+// adapter wastes tensor work, of which there is plenty, and no memory traffic,
+// which is what bounds both kernels.
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kStep = 32;       // contraction elements of one 16-byte load per lane
-constexpr int kMaxSplits = 32;  // parts of the first contraction
+constexpr int kWarps = 8, kThreads = 32 * kWarps;  // of the kernels for tall tiles
+constexpr int kLowWarps = 4;                       // of those for low ones
+constexpr int kStep = 32;      // contraction elements of one 16-byte load per lane
+constexpr int kTall = 64;      // rows of a tall tile
+constexpr int kMaxSplits = 8;  // CTAs of a cluster that share the first contraction
+
+// The parts of a sum that 16-bit operands hold.  bf16 has fp32's range: three
+// parts cut off (not rounded, so none overflows) hold all 24 bits.  fp16 parts
+// are of the sum times a power of two that brings the largest finite one of
+// its block (64 ranks of a row, or all where there are fewer) to [2^14, 2^15):
+// two rounded parts leave at most 2^-24 of a sum, or 2^-40 of the block's
+// largest where that is more.
+template <bool BF16>
+constexpr int kParts = BF16 ? 3 : 2;
 
 struct ApplyArgs {
   seedlm_adapters ad;
@@ -177,16 +187,17 @@ struct ApplyArgs {
   int64_t ldb;
   float* Y;
   int64_t ldy;
-  float* S;         // [splits][M][width], rows in sorted order
-  int splits;       // parts of the columns, one CTA each
-  int split_cols;   // columns of a part: a multiple of kStep
-  int width;        // slices * rank16
-  int rank16;       // rank rounded up to 16
-  int groups;       // first kernel: CTAs that share a slice's rank
+  uint16_t* S;      // [M][slices][kParts][slots], rows in sorted order
+  float* unscale;   // [M][slices][blocks]: takes fp16 parts back
+  int slots;        // ranks of a slice: 32, or rank rounded up to 64
+  int blocks;       // slots / 64, or 1
+  int split_cols;   // columns of one CTA of the first kernel's clusters
+  int groups;       // first kernel: CTAs that share a slice's (tall: all) ranks
   int chunk_first[SEEDLM_MAX_SLICES + 1];  // second kernel: chunks of outputs before each slice
   int chunk_rows;   // outputs of a chunk
   int slice_at[SEEDLM_MAX_SLICES];         // first output of each slice
-  int vec_a, vec_b, vec_y;  // rows can be read 16 bytes at a time: bit s for slice s
+  int vec_a, vec_b, vec_y;  // rows can be read 16 bytes at a time: bit s for slice s, bit
+                            // SEEDLM_MAX_SLICES of vec_a for X
 };
 
 __device__ __forceinline__ const int32_t* plan_tail_of(const ApplyArgs& p) { return p.plan + plan_tail(p.M, p.ad.n); }
@@ -212,10 +223,6 @@ __device__ __forceinline__ uint4 load8_slow(const uint16_t* row, int k, int len)
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ uint4 load8(const uint16_t* row, int k, int len, bool whole) {
-  return whole ? __ldg(reinterpret_cast<const uint4*>(row + k)) : load8_slow(row, k, len);
-}
-
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -236,124 +243,43 @@ __device__ __forceinline__ void mma_step(float (&d)[4], const uint4& lo, const u
   mma16816<BF16>(d, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
 }
 
-// S = s_a x A_a^T.  A CTA takes one tile of rows, RB blocks of 16 ranks of one
-// slice and one part of the columns; its warps take steps of the part in turn
-// (UNROLL at a time, all their loads in flight together) and add their sums
-// through shared memory in a fixed order.  The parts are added by the second
-// kernel.  NT: the tile's rows / 8.
-template <bool BF16, int NT, int RB, int UNROLL>
-__global__ void __launch_bounds__(kThreads) adapters_shrink_kernel(const __grid_constant__ ApplyArgs p) {
-  extern __shared__ float red[];  // [kWarps][RB * 16][NT * 8]
-  grid_wait();
-  // After the wait: what ran before this kernel is then complete for the next
-  // one too, which reads the plan, B and base before its own wait.
-  grid_launch_dependents();
-  if (!plan_fits(p)) return;
-  const int32_t* tail = plan_tail_of(p);
-  const int part = blockIdx.x % p.splits;
-  const int group = blockIdx.x / p.splits % p.groups;
-  const int s = blockIdx.x / (p.splits * p.groups) % p.ad.slices;
-  const int t = blockIdx.x / (p.splits * p.groups * p.ad.slices);
-  if (t >= tail[2]) return;
-  const int4 tile = reinterpret_cast<const int4*>(tail)[1 + t];
-  const int a = tile.x, first = tile.y, count = tile.z;
-  const int rank = rank_of(p.ad, a), r0 = group * RB * 16;
-  if (r0 >= rank) return;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
-  const int cols = p.ad.cols;
-  const uint16_t* A = static_cast<const uint16_t*>(p.ad.A[s]) + a * p.ad.a_adapter[s];
-  const int64_t a_row = p.ad.a_row[s];
-  const uint16_t* xrow[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const int at = 8 * i + g;
-    const int row = at < count ? p.plan[first + at] : -1;
-    xrow[i] = row >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, row, p.M) ? p.X + row * p.ldx : nullptr;
-  }
-  float acc[RB][NT][4] = {};
-  const int k0 = part * p.split_cols, k1 = min(cols, k0 + p.split_cols);
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  int k = k0 + warp * UNROLL * kStep;
-  if ((p.vec_a >> s) & 1) {
-    for (; k + UNROLL * kStep <= k1; k += kWarps * UNROLL * kStep) {
-      uint4 w[UNROLL][RB][2], x[UNROLL][NT];
-#pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
-        const int at = k + u * kStep + 8 * q;
-        const bool in = SEEDLM_IN_BOUNDS(g_check_flag, at + 7, cols);
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-          x[u][i] = in && xrow[i] ? __ldg(reinterpret_cast<const uint4*>(xrow[i] + at)) : zero;
-#pragma unroll
-        for (int b = 0; b < RB; ++b)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int r = r0 + 16 * b + 8 * h + g;
-            w[u][b][h] = in && r < rank ? ld_stream_u4(A + r * a_row + at) : zero;
-          }
-      }
-#pragma unroll
-      for (int u = 0; u < UNROLL; ++u)
-#pragma unroll
-        for (int b = 0; b < RB; ++b)
-#pragma unroll
-          for (int i = 0; i < NT; ++i) mma_step<BF16>(acc[b][i], w[u][b][0], w[u][b][1], x[u][i]);
-    }
-  }
-  // What is left of the part (all of it where rows are not aligned), a step at
-  // a time; elements beyond its end count as zero.
-  for (; k < k1; k += kWarps * UNROLL * kStep)
-    for (int u = 0; u < UNROLL && k + u * kStep < k1; ++u) {
-      const int at = k + u * kStep + 8 * q;
-      const bool whole = ((p.vec_a >> s) & 1) && k + (u + 1) * kStep <= k1;
-      uint4 w[RB][2];
-#pragma unroll
-      for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = r0 + 16 * b + 8 * h + g;
-          w[b][h] = r < rank ? load8(A + r * a_row, at, k1, whole) : zero;
-        }
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const uint4 x = xrow[i] ? load8(xrow[i], at, k1, whole) : zero;
-#pragma unroll
-        for (int b = 0; b < RB; ++b) mma_step<BF16>(acc[b][i], w[b][0], w[b][1], x);
-      }
-    }
-  // Sums of the warps, [rank][row], each warp's in its own place.
-  constexpr int T = NT * 8, R = RB * 16;
-  float* mine = red + warp * R * T;
-#pragma unroll
-  for (int b = 0; b < RB; ++b)
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      float* d = mine + (16 * b + g) * T + 8 * i + 2 * q;
-      *reinterpret_cast<float2*>(d) = make_float2(acc[b][i][0], acc[b][i][1]);
-      *reinterpret_cast<float2*>(d + 8 * T) = make_float2(acc[b][i][2], acc[b][i][3]);
-    }
-  __syncthreads();
-  const float scale = p.ad.scales ? p.ad.scales[a] : 1.f;
-  float* out = p.S + ((int64_t)part * p.M + first) * p.width + s * p.rank16 + r0;
-  SEEDLM_CHECK_ONLY(const int64_t out_extent = (int64_t)(p.splits - part) * p.M * p.width -
-                                               (int64_t)first * p.width - s * p.rank16 - r0;)
-  for (int e = threadIdx.x; e < R * T; e += kThreads) {
-    const int r = e % R, i = e / R;
-    if (i >= count || r0 + r >= rank) continue;
-    float sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += red[(w * R + r) * T + i];
-    if (SEEDLM_IN_BOUNDS(g_check_flag, (int64_t)i * p.width + r, out_extent)) out[(int64_t)i * p.width + r] = scale * sum;
-  }
+// Asynchronous copy of 16 bytes to shared memory, all but the first `bytes`
+// of them zero (with none, nothing is read).
+__device__ __forceinline__ void copy16(void* to, const void* from, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
-// The parts of S that a 16-bit operand holds.  bf16 has fp32's range: three
-// parts cut off (not rounded, so none overflows) hold all 24 bits.  fp16 parts
-// are of S times a power of two that brings the row's largest finite element
-// to [2^14, 2^15): two rounded parts leave at most 2^-24 of an element, or
-// 2^-40 of the largest one where that is more.
-template <bool BF16>
-constexpr int kParts = BF16 ? 3 : 2;
+// ---- the first kernel's end: the cluster's sums to S
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// All threads of all CTAs of the cluster; shared memory written before is
+// visible after.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ float2 load_of_cta(const float* mine, uint32_t cta) {
+  uint32_t at;
+  float2 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(cta));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
+}
 
 __device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
 
@@ -376,13 +302,294 @@ __device__ __forceinline__ void split(float v, uint16_t (&part)[3]) {
   }
 }
 
-// Elements of a row of a part of S in shared memory: an odd multiple of 32, so
-// that the 16-byte reads of 8 neighbouring lanes (2 rows x 4) touch every bank
-// once.
-__host__ __device__ inline int s_stride(int rank) { return ((rank + 31) / 32 | 1) * 32; }
+// sums[row][stride] of every CTA of the cluster, added in order and scaled, to
+// S: slots slot0 .. slot0 + N of the slices laid end to end.  The CTAs take the
+// rows in turn, a warp a row, a lane two neighbouring slots.
+template <bool BF16, int N>
+__device__ __forceinline__ void store_sums(const ApplyArgs& p, const float* sums, int stride, int first, int count,
+                                           int rank, int slot0, float scale) {
+  constexpr int P = kParts<BF16>;
+  const int lane = threadIdx.x % 32, warps = blockDim.x / 32, ctas = (int)cluster_size();
+  SEEDLM_CHECK_ONLY(const int64_t extent = (int64_t)p.M * p.ad.slices * P * p.slots;)
+  cluster_sync();
+  for (int i = (int)cluster_rank() + ctas * (threadIdx.x / 32); i < count; i += ctas * warps)
+#pragma unroll
+    for (int j0 = 0; j0 < N; j0 += 64) {
+      const int j = j0 + 2 * lane;
+      const int slot = slot0 + j, s = slot / p.slots, r = slot - s * p.slots;
+      const bool in = j < N && s < p.ad.slices;
+      float2 v = make_float2(0.f, 0.f);
+      if (in)
+        for (int c = 0; c < ctas; ++c) {
+          const float2 add = load_of_cta(sums + i * stride + j, c);
+          v = make_float2(v.x + add.x, v.y + add.y);
+        }
+      // Beyond the adapter's rank rows of zeros met x, which gives NaN where x
+      // has infinities.
+      v = make_float2(r < rank ? v.x * scale : 0.f, r + 1 < rank ? v.y * scale : 0.f);
+      float up = 1.f;
+      if constexpr (!BF16) {
+        float top = fmaxf(finite(v.x) ? fabsf(v.x) : 0.f, finite(v.y) ? fabsf(v.y) : 0.f);
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2)
+          if (2 * o < p.slots) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // 2^e with e = 14 - floor(log2 top), at most 126 (top below 2^-112).
+        const int e = top > 0.f ? min(126, 14 - ((int)(__float_as_uint(top) >> 23) - 127)) : 0;
+        up = __uint_as_float((uint32_t)(e + 127) << 23);
+        if (in && r % 64 == 0)
+          p.unscale[((int64_t)(first + i) * p.ad.slices + s) * p.blocks + r / 64] =
+              __uint_as_float((uint32_t)(127 - e) << 23);
+      }
+      uint16_t lo[3], hi[3];
+      split<BF16>(v.x * up, lo);
+      split<BF16>(v.y * up, hi);
+      const int64_t to = ((int64_t)(first + i) * p.ad.slices + s) * P * p.slots + r;
+#pragma unroll
+      for (int w = 0; w < P; ++w)
+        if (in && SEEDLM_IN_BOUNDS(g_check_flag, to + w * p.slots + 1, extent))
+          *reinterpret_cast<uint32_t*>(p.S + to + w * p.slots) = lo[w] | (uint32_t)hi[w] << 16;
+    }
+  cluster_sync();  // no CTA leaves while another reads its sums
+}
 
-__host__ __device__ inline int expand_smem(int rows, int rank, int parts) {
-  return parts * rows * s_stride(rank) * 2 + rows * 4;
+// S for low tiles (8 rows): bound by reading A.  A cluster takes one tile and
+// 16 RB ranks of one slice, each of its CTAs one part of the columns and each
+// warp 32 columns of that at a time.  Each warp keeps a ring of its next steps
+// coming into shared memory; a lane copies exactly what it will itself read, so
+// the ring needs no barrier.
+template <int RB>
+constexpr int kShrinkLowStages = RB == 4 ? 4 : 6;
+template <int RB>
+constexpr int kShrinkLowSmem = kLowWarps * kShrinkLowStages<RB> * (2 * RB + 1) * 512;
+
+template <bool BF16, int RB>
+__global__ void __launch_bounds__(32 * kLowWarps)
+adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  constexpr int kStages = kShrinkLowStages<RB>, kStageBytes = (2 * RB + 1) * 512, R = RB * 16;
+  grid_wait();
+  // After the wait: what ran before this kernel is then complete for the next
+  // one too, which reads the plan, B and base before its own wait.
+  grid_launch_dependents();
+  if (!plan_fits(p)) return;
+  const int32_t* tail = plan_tail_of(p);
+  const int cluster = blockIdx.x / (int)cluster_size();
+  const int group = cluster % p.groups, s = cluster / p.groups % p.ad.slices, t = cluster / (p.groups * p.ad.slices);
+  if (t >= tail[2]) return;
+  const int4 tile = reinterpret_cast<const int4*>(tail)[1 + t];
+  const int a = tile.x, first = tile.y, count = tile.z;
+  const int r0 = group * R, rank = rank_of(p.ad, a) - r0;  // of this group
+  if (rank <= 0) return;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
+  const int k0 = (int)cluster_rank() * p.split_cols, k1 = min(p.ad.cols, k0 + p.split_cols);
+  const bool vec = (p.vec_a >> s) & (p.vec_a >> SEEDLM_MAX_SLICES) & 1;
+  const int blocks = min(RB, (rank + 15) / 16);
+
+  // Row g of the tile and rows 8 j + g of A, at this lane's place in the part.
+  const int64_t a_row = p.ad.a_row[s];
+  const int row = g < count ? p.plan[first + g] : -1;
+  const bool have_x = row >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, row, p.M);
+  const int k_first = k0 + warp * kStep + 8 * q;
+  const uint16_t* x = p.X + (have_x ? row * p.ldx : 0) + k_first;
+  const uint16_t* A = static_cast<const uint16_t*>(p.ad.A[s]) + a * p.ad.a_adapter[s] + r0 * a_row + k_first;
+  unsigned char* ring = smem + warp * kStages * kStageBytes + lane * 16;
+  const int steps = k1 > k0 ? max(0, ((k1 - k0 + kStep - 1) / kStep - warp + kLowWarps - 1) / kLowWarps) : 0;
+  // Every copy of a step is made, those of rows that are not there with no
+  // bytes read and zeros written, so what is multiplied below needs no checks.
+  int left = k1 - k_first, fetched = 0;
+  unsigned char* to = ring;
+  auto fetch = [&]() {
+    if (fetched < steps) {
+      if (vec) {
+        const int have = max(0, min(16, 2 * left));
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+          if (b < blocks) {
+#pragma unroll
+            for (int j = 2 * b; j < 2 * b + 2; ++j) {
+              const int r = 8 * j + g;
+              copy16(to + j * 512, A + (r < rank ? r : 0) * a_row, r < rank ? have : 0);
+            }
+          }
+        copy16(to + 2 * RB * 512, x, have_x ? have : 0);
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < 2 * blocks; ++j)
+          *reinterpret_cast<uint4*>(to + j * 512) = load8_slow(A + (8 * j + g) * a_row, 0, 8 * j + g < rank ? left : 0);
+        *reinterpret_cast<uint4*>(to + 2 * RB * 512) = load8_slow(x, 0, have_x ? left : 0);
+      }
+      A += kLowWarps * kStep;
+      x += kLowWarps * kStep;
+      left -= kLowWarps * kStep;
+      to = to == ring + (kStages - 1) * kStageBytes ? ring : to + kStageBytes;
+      ++fetched;
+    }
+    copies_commit();
+  };
+  for (int i = 0; i < kStages - 1; ++i) fetch();
+  float acc[RB][4] = {};
+  const unsigned char* from = ring;
+  for (int step = 0; step < steps; ++step) {
+    copies_wait<kStages - 2>();
+    const uint4 v = *reinterpret_cast<const uint4*>(from + 2 * RB * 512);
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+      if (b < blocks)
+        mma_step<BF16>(acc[b], *reinterpret_cast<const uint4*>(from + 2 * b * 512),
+                       *reinterpret_cast<const uint4*>(from + (2 * b + 1) * 512), v);
+    from = from == ring + (kStages - 1) * kStageBytes ? ring : from + kStageBytes;
+    fetch();
+  }
+  // The warps' sums, [rank][9] (rows of 9 keep the reads off each other's
+  // banks), added in order into [row][R], all over the rings.
+  float* red = reinterpret_cast<float*>(smem);
+  float* sums = red + kLowWarps * R * 9;
+  static_assert((kLowWarps * R * 9 + 8 * R) * 4 <= kShrinkLowSmem<RB>, "the sums lie over the rings");
+  copies_wait<0>();
+  __syncthreads();
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) red[(warp * R + 16 * b + 8 * (e / 2) + g) * 9 + 2 * q + e % 2] = acc[b][e];
+  __syncthreads();
+  for (int e = threadIdx.x; e < R * count; e += 32 * kLowWarps) {
+    const int r = e % R, i = e / R;
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kLowWarps; ++w) sum += red[(w * R + r) * 9 + i];
+    sums[i * R + r] = sum;
+  }
+  store_sums<BF16, R>(p, sums, R, first, count, r0 + rank, s * p.slots + r0, p.ad.scales ? p.ad.scales[a] : 1.f);
+}
+
+// S for tall tiles (64 rows): a cluster takes one tile and NG slots of the
+// slices laid end to end, each of its CTAs one part of the columns.  Rows of X
+// and A come through a ring of shared-memory stages of 64 columns, and the
+// warps share the products out WR x WT, so that X is read once for NG slots and
+// no sums cross warps.  A row of a stage is 128 bytes, 8 units of 16; odd rows
+// have their halves swapped, so that 8 neighbouring lanes (2 rows x 4 units)
+// touch every bank once.
+constexpr int kStages = 4, kStageCols = 64;
+
+template <bool BF16, int NG, int WR>
+__global__ void __launch_bounds__(kThreads, 2) adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
+  constexpr int WT = kWarps / WR, RB = NG / 16 / WR, NT = kTall / 8 / WT;
+  static_assert(RB >= 1 && NT >= 1 && WR * RB * 16 == NG && WT * NT * 8 == kTall, "shares");
+  extern __shared__ __align__(128) unsigned char smem[];
+  constexpr int kStageRows = kTall + NG, kStageBytes = kStageRows * 128;
+  constexpr int kSumStride = NG + 4;
+  static_assert(kTall * kSumStride * 4 <= kStages * kStageBytes, "the sums lie over the stages");
+  grid_wait();
+  grid_launch_dependents();  // after the wait, as above
+  if (!plan_fits(p)) return;
+  const int32_t* tail = plan_tail_of(p);
+  const int cluster = blockIdx.x / (int)cluster_size();
+  const int group = cluster % p.groups, t = cluster / p.groups;
+  if (t >= tail[2]) return;
+  const int4 tile = reinterpret_cast<const int4*>(tail)[1 + t];
+  const int a = tile.x, first = tile.y, count = tile.z;
+  const int rank = rank_of(p.ad, a), cols = p.ad.cols;
+  const int k0 = (int)cluster_rank() * p.split_cols, k1 = min(cols, k0 + p.split_cols);
+  const int steps = k1 > k0 ? (k1 - k0 + kStageCols - 1) / kStageCols : 0;
+
+  // This thread's rows of every stage: unit `unit` of rows row0, row0 + 32, ...
+  constexpr int kMine = kStageRows * 8 / kThreads;
+  static_assert(kStageRows * 8 % kThreads == 0, "units");
+  const int unit = threadIdx.x % 8, row0 = threadIdx.x / 8;
+  const uint16_t* src[kMine];
+  unsigned vec = 0;
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int row = row0 + 32 * i;
+    src[i] = nullptr;
+    if (row < kTall) {
+      const int m = row < count ? p.plan[first + row] : -1;
+      if (m >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, m, p.M)) src[i] = p.X + m * p.ldx;
+      vec |= (unsigned)(p.vec_a >> SEEDLM_MAX_SLICES & 1) << i;
+    } else {
+      const int slot = group * NG + row - kTall, s = slot / p.slots, r = slot - s * p.slots;
+      if (s < p.ad.slices && r < rank) {
+        src[i] = static_cast<const uint16_t*>(p.ad.A[s]) + a * p.ad.a_adapter[s] + r * p.ad.a_row[s];
+        vec |= (unsigned)(p.vec_a >> s & 1) << i;
+      }
+    }
+  }
+  auto fetch = [&](int step) {
+    unsigned char* stage = smem + step % kStages * kStageBytes;
+    const int k = k0 + step * kStageCols + 8 * unit;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int row = row0 + 32 * i;
+      unsigned char* to = stage + row * 128 + (unit ^ (row & 1) * 4) * 16;
+      const int have = src[i] ? min(8, k1 - k) : 0;
+      if (have <= 0) *reinterpret_cast<uint4*>(to) = make_uint4(0u, 0u, 0u, 0u);
+      else if (vec >> i & 1) copy16(to, src[i] + k, 2 * have);
+      else *reinterpret_cast<uint4*>(to) = load8_slow(src[i], k, k1);
+    }
+  };
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (i < steps) fetch(i);
+    copies_commit();
+  }
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
+  const int r0 = warp % WR * RB * 16, t0 = warp / WR * NT * 8;
+  float acc[RB][NT][4] = {};
+  for (int step = 0; step < steps; ++step) {
+    copies_wait<kStages - 2>();
+    __syncthreads();  // the stage is there, and the one before it read by all
+    if (step + kStages - 1 < steps) fetch(step + kStages - 1);
+    copies_commit();
+    const unsigned char* stage = smem + step % kStages * kStageBytes;
+    // The tensor cores cut off what an addition leaves below the sum's last
+    // bit, so they only add up one stage; the stages are added in fp32, rounded.
+    float part_acc[RB][NT][4] = {};
+#pragma unroll
+    for (int c = 0; c < kStageCols / kStep; ++c) {
+      const int at = ((4 * c + q) ^ (g & 1) * 4) * 16;  // rows below differ from g by multiples of 8
+      uint4 w[RB][2];
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          w[b][h] = *reinterpret_cast<const uint4*>(stage + (kTall + r0 + 16 * b + 8 * h + g) * 128 + at);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(stage + (t0 + 8 * i + g) * 128 + at);
+#pragma unroll
+        for (int b = 0; b < RB; ++b) mma_step<BF16>(part_acc[b][i], w[b][0], w[b][1], x);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[b][i][e] += part_acc[b][i][e];
+  }
+  copies_wait<0>();
+  __syncthreads();  // the stages are read: the sums go over them
+  float* sums = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        sums[(t0 + 8 * i + 2 * q + e % 2) * kSumStride + r0 + 16 * b + 8 * (e / 2) + g] = acc[b][i][e];
+  store_sums<BF16, NG>(p, sums, kSumStride, first, count, rank, group * NG, p.ad.scales ? p.ad.scales[a] : 1.f);
+}
+
+// ---- the second kernel
+
+// A lane's four outputs of one row: to = from + d.
+__device__ __forceinline__ void add4_slow(float* to, const float* from, float4 d, int left) {
+  const float dv[4] = {d.x, d.y, d.z, d.w};
+  float b[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) b[j] = j < left ? __ldcg(from + j) : 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < left) to[j] = b[j] + dv[j];
 }
 
 // Y = base + S B_a^T.  A CTA takes one tile of rows and a chunk of one slice's
@@ -390,141 +597,373 @@ __host__ __device__ inline int expand_smem(int rows, int rank, int parts) {
 // outputs 4g .. 4g + 3 of rows 2q and 2q + 1 of every 8: the rows 4g + j of B
 // are dealt to the two 16-row operands so that base and Y are read and written
 // 16 bytes a lane, 128 bytes a row.
-template <bool BF16, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
-adapters_expand_kernel(const __grid_constant__ ApplyArgs p, int chunks, int in_place) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  constexpr int T = NT * 8, P = kParts<BF16>;
-  grid_launch_dependents();
-  if (!plan_fits(p)) {
-    grid_wait();
-    return;
-  }
+//
+// What a kernel reads besides S does not depend on the first kernel (which let
+// this one start only after everything before it had completed), so it is
+// requested before the wait for S.
+
+struct ExpandTile {
+  int a, first, count, rank, s, c0, c1;
+};
+
+// False if this CTA has nothing to do.
+__device__ __forceinline__ bool expand_tile(const ApplyArgs& p, int chunks, int in_place, ExpandTile& x) {
+  if (!plan_fits(p)) return false;
   const int32_t* tail = plan_tail_of(p);
   const int t = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-  int4 tile = make_int4(-1, 0, 0, 0);
-  if (t < tail[in_place ? 2 : 3]) tile = reinterpret_cast<const int4*>(tail)[1 + t];
-  const int a = tile.x, first = tile.y, count = tile.z;
-  const int rank = rank_of(p.ad, a);
-  if (count == 0 || (in_place && rank == 0)) {
+  if (t >= tail[in_place ? 2 : 3]) return false;
+  const int4 tile = reinterpret_cast<const int4*>(tail)[1 + t];
+  x.a = tile.x;
+  x.first = tile.y;
+  x.count = tile.z;
+  x.rank = rank_of(p.ad, x.a);
+  if (in_place && x.rank == 0) return false;
+  x.s = 0;
+  while (chunk >= p.chunk_first[x.s + 1]) ++x.s;
+  x.c0 = (chunk - p.chunk_first[x.s]) * p.chunk_rows;
+  x.c1 = min(p.ad.rows[x.s], x.c0 + p.chunk_rows);
+  return true;
+}
+
+// Low tiles (8 rows): bound by reading B.  Each warp keeps a ring of its next
+// outputs' rows of B and of base coming into shared memory, each lane copying
+// what it will itself read, and takes S straight into registers.  An item of
+// the ring is 32 outputs and a block of up to 64 ranks (32 KC); the last of an
+// output's items brings base.
+constexpr int kLowStages = 3;
+template <int KC>
+constexpr int kLowItemBytes = 2048 * KC + 1024;
+template <int KC>
+constexpr int kExpandLowSmem = kLowWarps * kLowStages * kLowItemBytes<KC>;
+
+template <bool BF16, int KC, bool MANY>
+__global__ void __launch_bounds__(32 * kLowWarps)
+adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int in_place) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  constexpr int P = kParts<BF16>, kItemBytes = kLowItemBytes<KC>, kRound = 32 * kLowWarps;
+  grid_launch_dependents();
+  ExpandTile x;
+  if (!expand_tile(p, chunks, in_place, x)) {
     grid_wait();
     return;
   }
-  int s = 0;
-  while (chunk >= p.chunk_first[s + 1]) ++s;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
-  const int stride = s_stride(p.ad.rank);
-  uint16_t* sp = reinterpret_cast<uint16_t*>(smem);           // [P][T][stride]
-  float* unscale = reinterpret_cast<float*>(sp + P * T * stride);  // [T]
-  const int rows = p.ad.rows[s];
-  const int c0 = (chunk - p.chunk_first[s]) * p.chunk_rows, c1 = min(rows, c0 + p.chunk_rows);
-  const uint16_t* B = static_cast<const uint16_t*>(p.ad.B[s]) + max(a, 0) * p.ad.b_adapter[s];
-  const int64_t b_row = p.ad.b_row[s];
-  const bool vec_b = (p.vec_b >> s) & 1, vec_y = (p.vec_y >> s) & 1;
-
-  // This lane's rows of base and Y; their numbers come from the plan.
-  int yrow[NT][2];
+  unsigned char* ring = smem + warp * kLowStages * kItemBytes + lane * 16;
+  const uint16_t* B = static_cast<const uint16_t*>(p.ad.B[x.s]) + max(x.a, 0) * p.ad.b_adapter[x.s];
+  const int64_t b_row = p.ad.b_row[x.s];
+  const bool vec_b = (p.vec_b >> x.s) & 1, vec_y = (p.vec_y >> x.s) & 1;
+  const float* from[2];
+  float* to[2];
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
+  for (int e = 0; e < 2; ++e) {
+    const int m = 2 * q + e < x.count ? p.plan[x.first + 2 * q + e] : -1;
+    const bool ok = m >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, m, p.M);
+    from[e] = ok ? p.base + m * p.ldb + p.slice_at[x.s] + 4 * g : nullptr;
+    to[e] = ok ? p.Y + m * p.ldy + p.slice_at[x.s] + 4 * g : nullptr;
+  }
+  const int groups = MANY ? max(1, (x.rank + 63) / 64) : 1;
+  const int first_n = x.c0 + 32 * warp;
+  const int items = first_n < x.c1 ? (x.c1 - first_n + kRound - 1) / kRound * groups : 0;
+  // The item to be fetched next: its outputs and its ranks.  As above, every
+  // copy of B is made, with no bytes where there is nothing to read.
+  const uint16_t* b_next = B + (first_n + 4 * g) * b_row + 8 * q;
+  int fetch_n = first_n, fetch_k = 0, fetched = 0;
+  unsigned char* into = ring;
+  int have[KC];
+  auto sizes = [&]() {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int at = 8 * i + 2 * q + e;
-      yrow[i][e] = at < count ? p.plan[first + at] : -1;
-      if (yrow[i][e] >= 0 && !SEEDLM_IN_BOUNDS(g_check_flag, yrow[i][e], p.M)) yrow[i][e] = -1;
-    }
-
-  grid_wait();
-  // S of the tile, its parts added in order, cut up for the tensor cores: a
-  // warp a row, two neighbouring elements a lane.
-  for (int i = warp; i < T; i += kWarps) {
-    float v[SEEDLM_MAX_RANK / 64][2];
-    float top = 0.f;
+    for (int c = 0; c < KC; ++c) have[c] = max(0, min(16, 2 * (x.rank - fetch_k - kStep * c - 8 * q)));
+  };
+  sizes();
+  auto fetch = [&]() {
+    if (fetched < items) {
+      const bool whole = fetch_n + 32 <= x.c1;
+      if (MANY) sizes();
+      if (vec_b && whole) {
+        const uint16_t* b = b_next;
 #pragma unroll
-    for (int j = 0; j < SEEDLM_MAX_RANK / 64; ++j) {
-      v[j][0] = v[j][1] = 0.f;
-      const int r = 64 * j + 2 * lane;
-      if (i < count && r < rank) {
-        const float* src = p.S + (int64_t)(first + i) * p.width + s * p.rank16 + r;
-        for (int part = 0; part < p.splits; ++part) {
-          const float2 add = __ldcg(reinterpret_cast<const float2*>(src + (int64_t)part * p.M * p.width));
-          v[j][0] += add.x;
-          if (r + 1 < rank) v[j][1] += add.y;
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+          for (int c = 0; c < KC; ++c) copy16(into + (4 * c + j) * 512, b + kStep * c, have[c]);
+          b += b_row;
         }
-        if (finite(v[j][0])) top = fmaxf(top, fabsf(v[j][0]));
-        if (finite(v[j][1])) top = fmaxf(top, fabsf(v[j][1]));
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int c = 0; c < KC; ++c)
+            *reinterpret_cast<uint4*>(into + (4 * c + j) * 512) =
+                load8_slow(b_next + j * b_row + kStep * c, 0,
+                           fetch_n + 4 * g + j < x.c1 ? x.rank - fetch_k - kStep * c - 8 * q : 0);
       }
+      b_next += 64;
+      fetch_k += 64;
+      if (!MANY || fetch_k >= x.rank) {  // the last ranks of these outputs
+        if (vec_y && whole) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (from[e]) copy16(into + kItemBytes - 1024 + e * 512, from[e] + fetch_n, 16);
+        }
+        b_next += kRound * b_row - 64 * groups;
+        fetch_n += kRound;
+        fetch_k = 0;
+      }
+      into = into == ring + (kLowStages - 1) * kItemBytes ? ring : into + kItemBytes;
+      ++fetched;
     }
-    float up = 1.f;
+    copies_commit();
+  };
+  for (int i = 0; i < kLowStages - 1; ++i) fetch();
+  grid_wait();
+  // Row g of S and its factors; rows that are not there, and rank 0, are zero.
+  const int64_t s_row = (int64_t)(x.first + g) * p.ad.slices + x.s;
+  const uint16_t* S = p.S + s_row * P * p.slots + 8 * q;
+  uint4 v[KC][P];
+  auto load_s = [&](int k) {
+#pragma unroll
+    for (int c = 0; c < KC; ++c)
+#pragma unroll
+      for (int pt = 0; pt < P; ++pt)
+        v[c][pt] = g < x.count && k + kStep * c < x.rank
+                       ? __ldcg(reinterpret_cast<const uint4*>(S + pt * p.slots + k + kStep * c))
+                       : make_uint4(0u, 0u, 0u, 0u);
+  };
+  float f[2] = {1.f, 1.f};
+  auto load_f = [&](int k) {
     if constexpr (!BF16) {
 #pragma unroll
-      for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // 2^e with e = 14 - floor(log2 top), at most 126 (top below 2^-112).
-      const int e = top > 0.f ? min(126, 14 - ((int)(__float_as_uint(top) >> 23) - 127)) : 0;
-      up = __uint_as_float((uint32_t)(e + 127) << 23);
-      if (lane == 0) unscale[i] = __uint_as_float((uint32_t)(127 - e) << 23);
+      for (int e = 0; e < 2; ++e)
+        if (2 * q + e < x.count && k < x.rank)
+          f[e] = __ldcg(p.unscale + ((int64_t)(x.first + 2 * q + e) * p.ad.slices + x.s) * p.blocks + k / 64);
     }
-#pragma unroll
-    for (int j = 0; j < SEEDLM_MAX_RANK / 64; ++j) {
-      const int r = 64 * j + 2 * lane;
-      if (r >= stride) continue;
-      uint16_t lo[3], hi[3];
-      split<BF16>(v[j][0] * up, lo);
-      split<BF16>(v[j][1] * up, hi);
-#pragma unroll
-      for (int w = 0; w < P; ++w)
-        *reinterpret_cast<uint32_t*>(sp + (w * T + i) * stride + r) = lo[w] | (uint32_t)hi[w] << 16;
+  };
+  load_s(0);
+  load_f(0);
+  float acc[2][4] = {}, total[2][4] = {};  // total: the blocks before this one, where there are many
+  int n0 = first_n, k = 0;
+  const unsigned char* item_at = ring;
+  for (int item = 0; item < items; ++item) {
+    if (MANY) {
+      load_s(k);
+      load_f(k);
     }
-  }
-  __syncthreads();
-
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  for (int n0 = c0 + 32 * warp; n0 < c1; n0 += 32 * kWarps) {
-    float acc[2][NT][4] = {};
-    for (int k = 0; k < rank; k += kStep) {
+    copies_wait<kLowStages - 2>();
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+      if (k + kStep * c >= x.rank) break;
       uint4 w[4];
-      const int at = k + 8 * q;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + 4 * g + j;
-        w[j] = zero;
-        if (n < c1) {
-          if (vec_b && at + 8 <= rank) w[j] = ld_stream_u4(B + n * b_row + at);
-          else if (at < rank) w[j] = load8_slow(B + n * b_row, at, rank);
+      for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint4*>(item_at + (4 * c + j) * 512);
+#pragma unroll
+      for (int pt = 0; pt < P; ++pt) {
+        mma_step<BF16>(acc[0], w[0], w[1], v[c][pt]);
+        mma_step<BF16>(acc[1], w[2], w[3], v[c][pt]);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        total[b][e] = fmaf(acc[b][e], f[e % 2], total[b][e]);
+        acc[b][e] = 0.f;
+      }
+    k += 64;
+    if (!MANY || k >= x.rank) {
+      const bool whole = vec_y && n0 + 32 <= x.c1;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (!to[e]) continue;
+        const float4 d = make_float4(total[0][e], total[0][2 + e], total[1][e], total[1][2 + e]);
+        if (whole) {
+          const float4 b = *reinterpret_cast<const float4*>(item_at + kItemBytes - 1024 + e * 512);
+          *reinterpret_cast<float4*>(to[e] + n0) = make_float4(b.x + d.x, b.y + d.y, b.z + d.z, b.w + d.w);
+        } else {
+          add4_slow(to[e] + n0, from[e] + n0, d, x.c1 - n0 - 4 * g);
         }
       }
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) total[b][e] = 0.f;
+      n0 += kRound;
+      k = 0;
+    }
+    item_at = item_at == ring + (kLowStages - 1) * kItemBytes ? ring : item_at + kItemBytes;
+    fetch();
+  }
+}
+
+// Tall tiles (64 rows): bound by reading base and writing Y.  Each warp has the
+// base of its next 32 outputs coming into shared memory while it multiplies (a
+// lane again copies what it will read), and the next step of B in registers.
+//
+// S lies in shared memory as RC steps of 32 ranks (1, 2, 4 or 8) for each part
+// and row; where RC is even, odd rows have the steps of a pair swapped, so that
+// the 16-byte reads of 8 neighbouring lanes (2 rows x 4) touch every bank once.
+template <bool BF16, int RC>
+constexpr int kExpandTallSmem = kWarps * 16 * 512 + kTall * 2 * 8 + kParts<BF16> * kTall * 32 * RC * 2 +
+                                kTall * ((RC + 1) / 2) * 4;
+
+template <bool BF16, int RC>
+__global__ void __launch_bounds__(kThreads, RC <= 2 ? 2 : 1)
+adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int in_place) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  constexpr int P = kParts<BF16>, T = kTall, NT = T / 8, kStride = 32 * RC, kRound = 32 * kWarps, kBlocks = (RC + 1) / 2;
+  grid_launch_dependents();
+  ExpandTile x;
+  if (!expand_tile(p, chunks, in_place, x)) {
+    grid_wait();
+    return;
+  }
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
+  unsigned char* ring = smem + warp * 16 * 512 + lane * 16;
+  int64_t* from_row = reinterpret_cast<int64_t*>(smem + kWarps * 16 * 512);  // [T] offsets into base, -1: no row
+  int64_t* to_row = from_row + T;                                            // [T] into Y
+  uint16_t* sp = reinterpret_cast<uint16_t*>(to_row + T);                    // [P][T][kStride]
+  float* unscale = reinterpret_cast<float*>(sp + P * T * kStride);           // [T][kBlocks]
+  const uint16_t* B = static_cast<const uint16_t*>(p.ad.B[x.s]) + max(x.a, 0) * p.ad.b_adapter[x.s];
+  const int64_t b_row = p.ad.b_row[x.s];
+  const bool vec_b = (p.vec_b >> x.s) & 1, vec_y = (p.vec_y >> x.s) & 1;
+  if (threadIdx.x < T) {
+    const int m = threadIdx.x < x.count ? p.plan[x.first + threadIdx.x] : -1;
+    const bool ok = m >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, m, p.M);
+    from_row[threadIdx.x] = ok ? m * p.ldb + p.slice_at[x.s] : -1;
+    to_row[threadIdx.x] = ok ? m * p.ldy + p.slice_at[x.s] : -1;
+  }
+  __syncthreads();
+  const bool full = x.count == T;
+  auto fetch = [&](int n0) {
+    if (vec_y && n0 + 32 <= x.c1) {
+      const float* base = p.base + n0 + 4 * g;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int64_t row = from_row[8 * i + 2 * q + e];
+          copy16(ring + (2 * i + e) * 512, base + max(row, (int64_t)0), row >= 0 ? 16 : 0);
+        }
+    }
+    copies_commit();
+  };
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  uint4 w[4], ahead[4];
+  const bool units = vec_b && x.rank % 8 == 0;
+  auto load_b = [&](int n0, int r) {
+    const uint16_t* b = B + (n0 + 4 * g) * b_row + r;
+    if (units && n0 + 32 <= x.c1) {
+      if (r < x.rank) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ahead[j] = __ldg(reinterpret_cast<const uint4*>(b + j * b_row));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ahead[j] = zero;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ahead[j] = load8_slow(b + j * b_row, 0, n0 + 4 * g + j < x.c1 ? x.rank - r : 0);
+    }
+  };
+  int n0 = x.c0 + 32 * warp;
+  load_b(n0, 8 * q);
+  grid_wait();
+  // The tile's S: units of 8 ranks; what lies beyond the last whole step of 32
+  // is not read below.
+  constexpr int kUnits = kStride / 8;
+  const int rank_units = (x.rank + kStep - 1) / kStep * (kStep / 8);
+  for (int u = threadIdx.x; u < P * T * kUnits; u += kThreads) {
+    const int r = u % kUnits, i = u / kUnits % T, pt = u / (kUnits * T);
+    if (r >= rank_units) continue;
+    const uint16_t* src = p.S + (((int64_t)(x.first + (i < x.count ? i : 0)) * p.ad.slices + x.s) * P + pt) * p.slots + 8 * r;
+    const int to = (pt * T + i) * kStride + 8 * (RC % 2 ? r : r ^ (i & 1) * 4);
+    copy16(sp + to, src, i < x.count ? 16 : 0);
+  }
+  if constexpr (!BF16)
+    for (int u = threadIdx.x; u < T * kBlocks; u += kThreads) {
+      const int i = u / kBlocks, b = u % kBlocks;
+      unscale[u] = i < x.count && 64 * b < x.rank
+                       ? __ldcg(p.unscale + ((int64_t)(x.first + i) * p.ad.slices + x.s) * p.blocks + b)
+                       : 0.f;
+    }
+  copies_commit();
+  fetch(n0);
+  copies_wait<1>();
+  __syncthreads();
+  const uint16_t* srow = sp + g * kStride;
+  const int swap = RC % 2 ? 0 : (g & 1) * kStep;
+  for (; n0 < x.c1; n0 += kRound) {
+    float acc[2][NT][4] = {};
+    float total[BF16 || kBlocks == 1 ? 1 : 2][NT][4] = {};  // fp16: the blocks before this one, where there are many
+#pragma unroll 1
+    for (int k = 0; k < x.rank; k += kStep) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = ahead[j];
+      const bool more = k + kStep < x.rank;
+      load_b(more ? n0 : n0 + kRound, (more ? k + kStep : 0) + 8 * q);
+      const uint16_t* from = srow + ((k + 8 * q) ^ swap);
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int pt = 0; pt < P; ++pt) {
-          const uint4 x = *reinterpret_cast<const uint4*>(sp + (pt * T + 8 * i + g) * stride + at);
-          mma_step<BF16>(acc[0][i], w[0], w[1], x);
-          mma_step<BF16>(acc[1][i], w[2], w[3], x);
+          const uint4 v = *reinterpret_cast<const uint4*>(from + (pt * T + 8 * i) * kStride);
+          mma_step<BF16>(acc[0][i], w[0], w[1], v);
+          mma_step<BF16>(acc[1][i], w[2], w[3], v);
+        }
+      if constexpr (!BF16 && kBlocks > 1) {
+        if (!more || k % 64 != 0)
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float f = unscale[(8 * i + 2 * q + e % 2) * kBlocks + k / 64];
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                total[b][i][e] = fmaf(acc[b][i][e], f, total[b][i][e]);
+                acc[b][i][e] = 0.f;
+              }
+            }
+      }
+    }
+    if constexpr (!BF16) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (kBlocks > 1) acc[b][i][e] = total[b][i][e];
+            else acc[b][i][e] *= unscale[8 * i + 2 * q + e % 2];
+          }
+    }
+    copies_wait<0>();
+    const bool whole = vec_y && n0 + 32 <= x.c1;
+    float* out = p.Y + n0 + 4 * g;
+    if (whole && full) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4 b = *reinterpret_cast<const float4*>(ring + (2 * i + e) * 512);
+          *reinterpret_cast<float4*>(out + to_row[8 * i + 2 * q + e]) =
+              make_float4(b.x + acc[0][i][e], b.y + acc[0][i][2 + e], b.z + acc[1][i][e], b.w + acc[1][i][2 + e]);
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = 8 * i + 2 * q + e;
+          const int64_t to = to_row[row];
+          if (to < 0) continue;
+          const float4 d = make_float4(acc[0][i][e], acc[0][i][2 + e], acc[1][i][e], acc[1][i][2 + e]);
+          if (whole) {
+            const float4 b = *reinterpret_cast<const float4*>(ring + (2 * i + e) * 512);
+            *reinterpret_cast<float4*>(out + to) = make_float4(b.x + d.x, b.y + d.y, b.z + d.z, b.w + d.w);
+          } else {
+            add4_slow(out + to, p.base + n0 + 4 * g + from_row[row], d, x.c1 - n0 - 4 * g);
+          }
         }
     }
-    const int n = n0 + 4 * g;
-    const int64_t col = p.slice_at[s] + n;
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (yrow[i][e] < 0 || n >= c1) continue;
-        float4 d = make_float4(acc[0][i][e], acc[0][i][2 + e], acc[1][i][e], acc[1][i][2 + e]);
-        if constexpr (!BF16) {
-          const float f = unscale[8 * i + 2 * q + e];
-          d = make_float4(d.x * f, d.y * f, d.z * f, d.w * f);
-        }
-        const float* from = p.base + yrow[i][e] * p.ldb + col;
-        float* to = p.Y + yrow[i][e] * p.ldy + col;
-        if (vec_y && n + 4 <= c1) {
-          const float4 b = __ldcg(reinterpret_cast<const float4*>(from));
-          *reinterpret_cast<float4*>(to) = make_float4(b.x + d.x, b.y + d.y, b.z + d.z, b.w + d.w);
-        } else {
-          const float dv[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (n + j < c1) to[j] = __ldcg(from + j) + dv[j];
-        }
-      }
+    fetch(n0 + kRound);
   }
 }
 
@@ -545,32 +984,34 @@ int launch_adapters_plan(int M, int n, const int32_t* ids, int32_t* plan, cudaSt
 
 namespace {
 
-// How the first product is shared out: RB blocks of 16 ranks to a CTA, the
-// columns in parts so that a few tiles still fill the GPU (about four CTAs an
-// SM), no part so short that a warp has less than one load.
+// How the first product is shared out: 16 `blocks` ranks of a slice to a cluster
+// of the low form, `ng` slots of all slices together to one of the tall form;
+// the columns in as many parts (CTAs of a cluster) as fill the GPU when there
+// are few tiles, none so short that its rings are not filled once.
 struct ShrinkShape {
-  int rank16, blocks, groups, splits, split_cols;
+  int slots, blocks, ng, groups, splits, split_cols;
 };
 
-// Steps of the columns whose loads a warp has in flight together: 12 loads of
-// 16 bytes a lane or so.
-constexpr int shrink_unroll(int nt, int blocks) { return nt == 1 ? 4 / blocks : 1; }
-
 ShrinkShape shrink_shape(const seedlm_adapters& ad, int M, const DeviceInfo& dev) {
-  ShrinkShape sh;
-  sh.rank16 = (ad.rank + 15) / 16 * 16;
-  const bool low = adapter_tile_rows(M) == 8;
-  const int blocks16 = sh.rank16 / 16;
-  sh.blocks = blocks16 >= 4 && low ? 4 : blocks16 >= 2 ? 2 : 1;
-  sh.groups = (blocks16 + sh.blocks - 1) / sh.blocks;
-  const int64_t ctas = max_tiles(M, ad.n) * sh.groups * ad.slices;
+  ShrinkShape sh{};
+  sh.slots = ad.rank <= 32 ? 32 : (ad.rank + 63) / 64 * 64;
+  int64_t clusters = max_tiles(M, ad.n), round;
+  if (adapter_tile_rows(M) == 8) {
+    sh.blocks = sh.slots == 32 ? 2 : 4;
+    sh.groups = sh.slots / (16 * sh.blocks);
+    clusters *= sh.groups * ad.slices;
+    round = kLowWarps * 4;
+  } else {
+    const int width = ad.slices * sh.slots;
+    sh.ng = width > 64 ? 128 : width > 32 ? 64 : 32;
+    sh.groups = (width + sh.ng - 1) / sh.ng;
+    clusters *= sh.groups;
+    round = kStages * kStageCols / kStep;
+  }
   const int64_t steps = (ad.cols + kStep - 1) / kStep;
-  const int64_t round = kWarps * shrink_unroll(low ? 1 : 8, sh.blocks);
-  int64_t splits = (4 * (int64_t)dev.num_sms + ctas - 1) / ctas;
-  if (splits > kMaxSplits) splits = kMaxSplits;
-  const int64_t each = std::max<int64_t>(1, ((steps + splits - 1) / splits + round - 1) / round) * round;
-  sh.split_cols = (int)(each * kStep);
-  sh.splits = (int)std::max<int64_t>(1, (steps + each - 1) / each);
+  sh.splits = 1;
+  while (sh.splits < kMaxSplits && sh.splits * clusters < 3 * dev.num_sms && steps >= 2 * sh.splits * round) sh.splits *= 2;
+  sh.split_cols = (int)((steps + sh.splits - 1) / sh.splits * kStep);
   return sh;
 }
 
@@ -578,50 +1019,91 @@ bool rows_aligned(const void* p, int64_t ld1, int64_t ld2, int bytes) {
   return aligned(p, 16) && ld1 * bytes % 16 == 0 && ld2 * bytes % 16 == 0;
 }
 
-template <bool BF16, int NT, int RB>
-int launch_shrink(const ApplyArgs& p, int64_t tiles, cudaStream_t stream, const DeviceInfo& dev) {
-  auto kernel = adapters_shrink_kernel<BF16, NT, RB, shrink_unroll(NT, RB)>;
-  const size_t smem = (size_t)kWarps * RB * 16 * NT * 8 * sizeof(float);
-  int rc = allow_max_smem((const void*)kernel, dev);
-  if (rc) return rc;
-  return launch_pdl(kernel, (unsigned)(tiles * p.ad.slices * p.groups * p.splits), kThreads, smem, stream, p);
+template <class Kernel, class... Args>
+int launch_products_kernel(Kernel kernel, int64_t grid, int threads, int smem, int cluster, cudaStream_t stream,
+                           const DeviceInfo& dev, const Args&... args) {
+  const int rc = allow_max_smem((const void*)kernel, dev);
+  return rc ? rc : launch_pdl_cluster(kernel, (unsigned)grid, threads, (size_t)smem, cluster, stream, args...);
 }
 
-template <bool BF16, int NT>
+template <bool BF16, int RB>
+int launch_shrink_low(const ApplyArgs& p, int64_t tiles, int splits, cudaStream_t stream, const DeviceInfo& dev) {
+  return launch_products_kernel(adapters_shrink_low_kernel<BF16, RB>, tiles * p.ad.slices * p.groups * splits,
+                                32 * kLowWarps, kShrinkLowSmem<RB>, splits, stream, dev, p);
+}
+
+template <bool BF16, int NG, int WR>
+int launch_shrink_tall(const ApplyArgs& p, int64_t tiles, int splits, cudaStream_t stream, const DeviceInfo& dev) {
+  return launch_products_kernel(adapters_shrink_tall_kernel<BF16, NG, WR>, tiles * p.groups * splits, kThreads,
+                                kStages * (kTall + NG) * 128, splits, stream, dev, p);
+}
+
+template <bool BF16, int KC, bool MANY>
+int launch_expand_low(const ApplyArgs& p, int64_t grid, int chunks, cudaStream_t stream, const DeviceInfo& dev) {
+  return launch_products_kernel(adapters_expand_low_kernel<BF16, KC, MANY>, grid, 32 * kLowWarps, kExpandLowSmem<KC>, 1,
+                                stream, dev, p, chunks, (int)(p.base == p.Y));
+}
+
+template <bool BF16, int RC>
+int launch_expand_tall(const ApplyArgs& p, int64_t grid, int chunks, cudaStream_t stream, const DeviceInfo& dev) {
+  return launch_products_kernel(adapters_expand_tall_kernel<BF16, RC>, grid, kThreads, kExpandTallSmem<BF16, RC>, 1,
+                                stream, dev, p, chunks, (int)(p.base == p.Y));
+}
+
+template <bool BF16>
 int launch_products(ApplyArgs& p, const ShrinkShape& sh, int64_t tiles, cudaStream_t stream, const DeviceInfo& dev) {
+  const bool low = sh.ng == 0;
   int rc;
-  if (NT == 1 && sh.blocks == 4) rc = launch_shrink<BF16, 1, 4>(p, tiles, stream, dev);
-  else if (sh.blocks == 2) rc = launch_shrink<BF16, NT, 2>(p, tiles, stream, dev);
-  else rc = launch_shrink<BF16, NT, 1>(p, tiles, stream, dev);
+  if (low)
+    rc = sh.blocks == 4 ? launch_shrink_low<BF16, 4>(p, tiles, sh.splits, stream, dev)
+                        : launch_shrink_low<BF16, 2>(p, tiles, sh.splits, stream, dev);
+  else
+    rc = sh.ng == 128  ? launch_shrink_tall<BF16, 128, 4>(p, tiles, sh.splits, stream, dev)
+         : sh.ng == 64 ? launch_shrink_tall<BF16, 64, 4>(p, tiles, sh.splits, stream, dev)
+                       : launch_shrink_tall<BF16, 32, 2>(p, tiles, sh.splits, stream, dev);
   if (rc) return rc;
-  // Chunks of outputs: as long as they can be (a CTA pays for its S once) with
-  // some eight CTAs left for each SM, at least one round of its warps.
+  // Chunks of outputs: as long as they can be (a CTA fetches its S once) with
+  // enough CTAs left for several rounds of the GPU, at least one round of the
+  // CTA's warps.
   int64_t total = 0;
   for (int s = 0; s < p.ad.slices; ++s) total += p.ad.rows[s];
-  const int round = 32 * kWarps;
-  int64_t rounds = total * tiles / ((int64_t)round * 8 * dev.num_sms);
-  rounds = rounds < 1 ? 1 : rounds > 8 ? 8 : rounds;
+  const int round = 32 * (low ? kLowWarps : kWarps);
+  int64_t rounds = total * tiles / ((int64_t)round * (low ? 12 : 8) * dev.num_sms);
+  rounds = rounds < 1 ? 1 : rounds > 16 ? 16 : rounds;
   p.chunk_rows = (int)rounds * round;
-  int chunks = 0, at = 0;
+  int64_t chunks = 0;
+  int at = 0;
   for (int s = 0; s < p.ad.slices; ++s) {
-    p.chunk_first[s] = chunks;
+    p.chunk_first[s] = (int)chunks;
     p.slice_at[s] = at;
     chunks += (p.ad.rows[s] + p.chunk_rows - 1) / p.chunk_rows;
     at += p.ad.rows[s];
   }
-  for (int s = p.ad.slices; s <= SEEDLM_MAX_SLICES; ++s) p.chunk_first[s] = chunks;
-  if (chunks * tiles > INT32_MAX) return SEEDLM_EUNSUPPORTED;
-  auto kernel = adapters_expand_kernel<BF16, NT>;
-  if ((rc = allow_max_smem((const void*)kernel, dev))) return rc;
-  return launch_pdl(kernel, (unsigned)(chunks * tiles), kThreads, expand_smem(NT * 8, p.ad.rank, kParts<BF16>), stream,
-                    p, chunks, (int)(p.base == p.Y));
+  for (int s = p.ad.slices; s <= SEEDLM_MAX_SLICES; ++s) p.chunk_first[s] = (int)chunks;
+  const int64_t grid = chunks * tiles;
+  if (grid > INT32_MAX) return SEEDLM_EUNSUPPORTED;
+  if (low)
+    return p.slots == 32   ? launch_expand_low<BF16, 1, false>(p, grid, (int)chunks, stream, dev)
+           : p.slots == 64 ? launch_expand_low<BF16, 2, false>(p, grid, (int)chunks, stream, dev)
+                           : launch_expand_low<BF16, 2, true>(p, grid, (int)chunks, stream, dev);
+  return p.slots == 32    ? launch_expand_tall<BF16, 1>(p, grid, (int)chunks, stream, dev)
+         : p.slots == 64  ? launch_expand_tall<BF16, 2>(p, grid, (int)chunks, stream, dev)
+         : p.slots == 128 ? launch_expand_tall<BF16, 4>(p, grid, (int)chunks, stream, dev)
+                          : launch_expand_tall<BF16, 8>(p, grid, (int)chunks, stream, dev);
+}
+
+// Bytes of S, then those of its factors.
+int64_t sums_bytes(const seedlm_adapters& ad, int M, int slots) {
+  const int parts = ad.dtype == SEEDLM_BF16 ? kParts<true> : kParts<false>;
+  return (int64_t)M * ad.slices * parts * slots * 2;
 }
 
 }  // namespace
 
 int64_t adapters_workspace_bytes(const seedlm_adapters& ad, int M, const DeviceInfo& dev) {
   const ShrinkShape sh = shrink_shape(ad, M, dev);
-  return (int64_t)sh.splits * M * ad.slices * sh.rank16 * 4;
+  const int64_t blocks = std::max(1, sh.slots / 64);
+  return sums_bytes(ad, M, sh.slots) + (ad.dtype == SEEDLM_F16 ? (int64_t)M * ad.slices * blocks * 4 : 0);
 }
 
 int launch_adapters_apply(const seedlm_adapters& ad, const int32_t* plan, int M, const uint16_t* X, int64_t ldx,
@@ -638,25 +1120,24 @@ int launch_adapters_apply(const seedlm_adapters& ad, const int32_t* plan, int M,
   p.ldb = ldb;
   p.Y = Y;
   p.ldy = ldy;
-  p.S = static_cast<float*>(workspace);
-  p.splits = sh.splits;
+  p.S = static_cast<uint16_t*>(workspace);
+  p.unscale = reinterpret_cast<float*>(static_cast<char*>(workspace) + sums_bytes(ad, M, sh.slots));
+  p.slots = sh.slots;
+  p.blocks = std::max(1, sh.slots / 64);
   p.split_cols = sh.split_cols;
-  p.rank16 = sh.rank16;
-  p.width = ad.slices * sh.rank16;
   p.groups = sh.groups;
   int64_t at = 0;
   for (int s = 0; s < ad.slices; ++s) {
-    p.vec_a |= (rows_aligned(ad.A[s], ad.a_adapter[s], ad.a_row[s], 2) && rows_aligned(X, ldx, 0, 2)) << s;
+    p.vec_a |= rows_aligned(ad.A[s], ad.a_adapter[s], ad.a_row[s], 2) << s;
     p.vec_b |= rows_aligned(ad.B[s], ad.b_adapter[s], ad.b_row[s], 2) << s;
     p.vec_y |= (rows_aligned(base, ldb, at, 4) && rows_aligned(Y, ldy, at, 4)) << s;
     at += ad.rows[s];
   }
+  p.vec_a |= rows_aligned(X, ldx, 0, 2) << SEEDLM_MAX_SLICES;
   const int64_t tiles = max_tiles(M, ad.n);
   if (tiles * ad.slices * sh.groups * sh.splits > INT32_MAX) return SEEDLM_EUNSUPPORTED;
-  const bool bf16 = ad.dtype == SEEDLM_BF16;
-  if (adapter_tile_rows(M) == 8)
-    return bf16 ? launch_products<true, 1>(p, sh, tiles, stream, dev) : launch_products<false, 1>(p, sh, tiles, stream, dev);
-  return bf16 ? launch_products<true, 8>(p, sh, tiles, stream, dev) : launch_products<false, 8>(p, sh, tiles, stream, dev);
+  return ad.dtype == SEEDLM_BF16 ? launch_products<true>(p, sh, tiles, stream, dev)
+                                 : launch_products<false>(p, sh, tiles, stream, dev);
 }
 
 int read_and_clear_plan_mismatch(unsigned int* out) {

@@ -22,17 +22,21 @@ __device__ __forceinline__ void grid_launch_dependents() {
 }
 
 template <class... Params, class... Args>
-int launch_pdl(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args&&... args) {
+int launch_pdl_cluster(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+                       Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
   if (err != cudaSuccess) {
     cudaGetLastError();  // the caller has the error; the next call starts clean
@@ -40,6 +44,11 @@ int launch_pdl(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, c
   }
   count_launch();
   return SEEDLM_OK;
+}
+
+template <class... Params, class... Args>
+int launch_pdl(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args&&... args) {
+  return launch_pdl_cluster(kernel, grid, threads, smem, 1, stream, std::forward<Args>(args)...);
 }
 
 }  // namespace seedlm
