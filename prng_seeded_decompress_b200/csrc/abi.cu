@@ -440,6 +440,8 @@ int seedlm_device_error(int* flag) {
   if (v) out |= 1;
   if ((rc = read_and_clear_amort_error(&v))) return rc;
   if (v) out |= 1;
+  if ((rc = read_and_clear_adapters_error(&v))) return rc;
+  if (v) out |= 1;
   // Bounds violations recorded by a checked build (always 0 otherwise).
   int (*const readers[])(unsigned int*) = {read_and_clear_check_gemv, read_and_clear_check_decompress,
                                            read_and_clear_check_gemm_tc, read_and_clear_check_encode,

@@ -10,6 +10,7 @@
 #include "launch.cuh"
 #include "seedlm_device.cuh"
 #include "seedlm_internal.h"
+#include "tcgen05.cuh"
 
 namespace seedlm {
 
@@ -19,6 +20,8 @@ namespace {
 
 // Set when a plan does not belong to the call it is given to.
 __device__ unsigned int g_plan_mismatch;
+// Set when a kernel gave up waiting for its own products.
+__device__ unsigned int g_wait_error;
 
 // ---------------------------------------------------------------- the plan
 //
@@ -236,11 +239,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One step of 32: rows g and g + 8 of the 16-row operand in lo and hi.
+// Half a step of 32: rows g and g + 8 of the 16-row operand in lo and hi.  The
+// halves of several sums are issued in turn, so that no product waits for the
+// one before it.
 template <bool BF16>
-__device__ __forceinline__ void mma_step(float (&d)[4], const uint4& lo, const uint4& hi, const uint4& x) {
-  mma16816<BF16>(d, lo.x, hi.x, lo.y, hi.y, x.x, x.y);
-  mma16816<BF16>(d, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
+__device__ __forceinline__ void mma_half(int half, float (&d)[4], const uint4& lo, const uint4& hi, const uint4& x) {
+  if (half == 0) mma16816<BF16>(d, lo.x, hi.x, lo.y, hi.y, x.x, x.y);
+  else mma16816<BF16>(d, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
 }
 
 // Asynchronous copy of 16 bytes to shared memory, all but the first `bytes`
@@ -248,6 +253,14 @@ __device__ __forceinline__ void mma_step(float (&d)[4], const uint4& lo, const u
 __device__ __forceinline__ void copy16(void* to, const void* from, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
                "r"(bytes)
+               : "memory");
+}
+// The same where a row's neighbours in its 128-byte line are not wanted: the L2
+// then fetches 64 bytes of it, not the line (measured: half the DRAM traffic
+// for rows of up to 64 bytes in every 128).
+__device__ __forceinline__ void copy16_short(void* to, const void* from, int bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -432,11 +445,18 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
   for (int step = 0; step < steps; ++step) {
     copies_wait<kStages - 2>();
     const uint4 v = *reinterpret_cast<const uint4*>(from + 2 * RB * 512);
+    uint4 w[2 * RB];
 #pragma unroll
     for (int b = 0; b < RB; ++b)
-      if (b < blocks)
-        mma_step<BF16>(acc[b], *reinterpret_cast<const uint4*>(from + 2 * b * 512),
-                       *reinterpret_cast<const uint4*>(from + (2 * b + 1) * 512), v);
+      if (b < blocks) {
+        w[2 * b] = *reinterpret_cast<const uint4*>(from + 2 * b * 512);
+        w[2 * b + 1] = *reinterpret_cast<const uint4*>(from + (2 * b + 1) * 512);
+      }
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+        if (b < blocks) mma_half<BF16>(half, acc[b], w[2 * b], w[2 * b + 1], v);
     from = from == ring + (kStages - 1) * kStageBytes ? ring : from + kStageBytes;
     fetch();
   }
@@ -496,36 +516,51 @@ __global__ void __launch_bounds__(kThreads, 2) adapters_shrink_tall_kernel(const
   constexpr int kMine = kStageRows * 8 / kThreads;
   static_assert(kStageRows * 8 % kThreads == 0, "units");
   const int unit = threadIdx.x % 8, row0 = threadIdx.x / 8;
-  const uint16_t* src[kMine];
+  const uint16_t* src[kMine];  // at this thread's place in the stage to be fetched next
+  int bytes[kMine];            // 16, or 0 where there is no such row
   unsigned vec = 0;
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
     const int row = row0 + 32 * i;
-    src[i] = nullptr;
+    src[i] = p.X;
+    bytes[i] = 0;
+    bool aligned16 = true;
     if (row < kTall) {
       const int m = row < count ? p.plan[first + row] : -1;
-      if (m >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, m, p.M)) src[i] = p.X + m * p.ldx;
-      vec |= (unsigned)(p.vec_a >> SEEDLM_MAX_SLICES & 1) << i;
+      if (m >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, m, p.M)) {
+        src[i] = p.X + m * p.ldx;
+        bytes[i] = 16;
+        aligned16 = p.vec_a >> SEEDLM_MAX_SLICES & 1;
+      }
     } else {
       const int slot = group * NG + row - kTall, s = slot / p.slots, r = slot - s * p.slots;
       if (s < p.ad.slices && r < rank) {
         src[i] = static_cast<const uint16_t*>(p.ad.A[s]) + a * p.ad.a_adapter[s] + r * p.ad.a_row[s];
-        vec |= (unsigned)(p.vec_a >> s & 1) << i;
+        bytes[i] = 16;
+        aligned16 = p.vec_a >> s & 1;
       }
     }
+    vec |= (unsigned)aligned16 << i;
+    src[i] += bytes[i] ? k0 + 8 * unit : 0;
   }
+  const bool all_vec = vec == (1u << kMine) - 1;
   auto fetch = [&](int step) {
-    unsigned char* stage = smem + step % kStages * kStageBytes;
-    const int k = k0 + step * kStageCols + 8 * unit;
+    unsigned char* to = smem + step % kStages * kStageBytes + row0 * 128 + (unit ^ (row0 & 1) * 4) * 16;
+    const int left = k1 - k0 - step * kStageCols - 8 * unit;
+    if (all_vec && left >= 8) {
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      const int row = row0 + 32 * i;
-      unsigned char* to = stage + row * 128 + (unit ^ (row & 1) * 4) * 16;
-      const int have = src[i] ? min(8, k1 - k) : 0;
-      if (have <= 0) *reinterpret_cast<uint4*>(to) = make_uint4(0u, 0u, 0u, 0u);
-      else if (vec >> i & 1) copy16(to, src[i] + k, 2 * have);
-      else *reinterpret_cast<uint4*>(to) = load8_slow(src[i], k, k1);
+      for (int i = 0; i < kMine; ++i) copy16(to + i * 4096, src[i], bytes[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int have = bytes[i] ? min(8, left) : 0;
+        if (have <= 0) *reinterpret_cast<uint4*>(to + i * 4096) = make_uint4(0u, 0u, 0u, 0u);
+        else if (vec >> i & 1) copy16(to + i * 4096, src[i], 2 * have);
+        else *reinterpret_cast<uint4*>(to + i * 4096) = load8_slow(src[i], 0, left);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) src[i] += kStageCols;
   };
   for (int i = 0; i < kStages - 1; ++i) {
     if (i < steps) fetch(i);
@@ -552,12 +587,15 @@ __global__ void __launch_bounds__(kThreads, 2) adapters_shrink_tall_kernel(const
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           w[b][h] = *reinterpret_cast<const uint4*>(stage + (kTall + r0 + 16 * b + 8 * h + g) * 128 + at);
+      uint4 x[NT];
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const uint4 x = *reinterpret_cast<const uint4*>(stage + (t0 + 8 * i + g) * 128 + at);
+      for (int i = 0; i < NT; ++i) x[i] = *reinterpret_cast<const uint4*>(stage + (t0 + 8 * i + g) * 128 + at);
 #pragma unroll
-        for (int b = 0; b < RB; ++b) mma_step<BF16>(part_acc[b][i], w[b][0], w[b][1], x);
-      }
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int b = 0; b < RB; ++b) mma_half<BF16>(half, part_acc[b][i], w[b][0], w[b][1], x[i]);
     }
 #pragma unroll
     for (int b = 0; b < RB; ++b)
@@ -684,7 +722,7 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
 #pragma unroll
-          for (int c = 0; c < KC; ++c) copy16(into + (4 * c + j) * 512, b + kStep * c, have[c]);
+          for (int c = 0; c < KC; ++c) copy16_short(into + (4 * c + j) * 512, b + kStep * c, have[c]);
           b += b_row;
         }
       } else {
@@ -739,7 +777,7 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
   };
   load_s(0);
   load_f(0);
-  float acc[2][4] = {}, total[2][4] = {};  // total: the blocks before this one, where there are many
+  float total[2][4] = {};
   int n0 = first_n, k = 0;
   const unsigned char* item_at = ring;
   for (int item = 0; item < items; ++item) {
@@ -748,6 +786,7 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
       load_f(k);
     }
     copies_wait<kLowStages - 2>();
+    float acc[P][2][4] = {};
 #pragma unroll
     for (int c = 0; c < KC; ++c) {
       if (k + kStep * c >= x.rank) break;
@@ -755,17 +794,22 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
 #pragma unroll
       for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint4*>(item_at + (4 * c + j) * 512);
 #pragma unroll
-      for (int pt = 0; pt < P; ++pt) {
-        mma_step<BF16>(acc[0], w[0], w[1], v[c][pt]);
-        mma_step<BF16>(acc[1], w[2], w[3], v[c][pt]);
-      }
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int pt = 0; pt < P; ++pt) {
+          mma_half<BF16>(half, acc[pt][0], w[0], w[1], v[c][pt]);
+          mma_half<BF16>(half, acc[pt][1], w[2], w[3], v[c][pt]);
+        }
     }
+    // The parts from the smallest on, then the blocks before this one.
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        total[b][e] = fmaf(acc[b][e], f[e % 2], total[b][e]);
-        acc[b][e] = 0.f;
+        float sum = acc[P - 1][b][e];
+#pragma unroll
+        for (int pt = P - 2; pt >= 0; --pt) sum += acc[pt][b][e];
+        total[b][e] = fmaf(sum, f[e % 2], total[b][e]);
       }
     k += 64;
     if (!MANY || k >= x.rank) {
@@ -793,177 +837,209 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
   }
 }
 
-// Tall tiles (64 rows): bound by reading base and writing Y.  Each warp has the
-// base of its next 32 outputs coming into shared memory while it multiplies (a
-// lane again copies what it will read), and the next step of B in registers.
-//
-// S lies in shared memory as RC steps of 32 ranks (1, 2, 4 or 8) for each part
-// and row; where RC is even, odd rows have the steps of a pair swapped, so that
-// the 16-byte reads of 8 neighbouring lanes (2 rows x 4) touch every bank once.
-template <bool BF16, int RC>
-constexpr int kExpandTallSmem = kWarps * 16 * 512 + kTall * 2 * 8 + kParts<BF16> * kTall * 32 * RC * 2 +
-                                kTall * ((RC + 1) / 2) * 4;
+// Tall tiles (64 rows): bound by reading base and writing Y, so the products are
+// left to tcgen05.mma: 128 outputs (rows of B) by the tile's 64 rows, every part
+// of S against the same B, summed in tensor memory, two sums in turn.  B comes
+// through a ring of shared-memory stages.  A thread takes one output of all rows
+// from tensor memory, so that a warp's reads of base and writes of Y are 128
+// bytes of one row; it has asked for the base of its 64 outputs before it waits
+// for the products.  NB: blocks of 64 ranks; fp16 parts are scaled block by
+// block, so there each block has a sum of its own.
+template <bool BF16, int NB>
+struct TallLayout {
+  static constexpr int P = kParts<BF16>, kThreads = 128, kOutputs = 128;
+  static constexpr int kStages = NB == 4 ? 2 : 3;
+  static constexpr int kSums = BF16 ? 1 : NB;           // 64 columns of tensor memory each
+  static constexpr int kColumns = 2 * kSums * kTall;
+  static constexpr int kB = P * NB * kTall * 128;       // after S[P][NB][64 rows of 128 bytes]
+  static constexpr int kStageBytes = NB * kOutputs * 128;
+  static constexpr int kRows = kB + kStages * kStageBytes;  // from_row, to_row
+  static constexpr int kScales = kRows + 2 * kTall * 8;     // fp16: unscale[NB][64]
+  static constexpr int kBars = kScales + (BF16 ? 0 : NB * kTall * 4);
+  static constexpr int kBytes = kBars + 2 * 8 + 8;          // two barriers, tensor memory's address, give-up flag
+};
+// A product of one tile takes microseconds; a wait this long never ends.
+constexpr uint64_t kTallWaitLimit = 2000000000ull;
 
-template <bool BF16, int RC>
-__global__ void __launch_bounds__(kThreads, RC <= 2 ? 2 : 1)
+template <bool BF16, int NB>
+__global__ void __launch_bounds__(128, NB == 1 ? 3 : 1)
 adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int in_place) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  constexpr int P = kParts<BF16>, T = kTall, NT = T / 8, kStride = 32 * RC, kRound = 32 * kWarps, kBlocks = (RC + 1) / 2;
-  grid_launch_dependents();
+  using L = TallLayout<BF16, NB>;
+  constexpr int P = L::P, T = kTall, kOut = L::kOutputs, kSt = L::kStages;
+  extern __shared__ __align__(1024) unsigned char smem[];
   ExpandTile x;
   if (!expand_tile(p, chunks, in_place, x)) {
     grid_wait();
     return;
   }
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
-  unsigned char* ring = smem + warp * 16 * 512 + lane * 16;
-  int64_t* from_row = reinterpret_cast<int64_t*>(smem + kWarps * 16 * 512);  // [T] offsets into base, -1: no row
-  int64_t* to_row = from_row + T;                                            // [T] into Y
-  uint16_t* sp = reinterpret_cast<uint16_t*>(to_row + T);                    // [P][T][kStride]
-  float* unscale = reinterpret_cast<float*>(sp + P * T * kStride);           // [T][kBlocks]
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  int64_t* from_row = reinterpret_cast<int64_t*>(smem + L::kRows);
+  int64_t* to_row = from_row + T;
+  const uint32_t done = tc::smem_u32(smem + L::kBars);
+  volatile uint32_t* slot = reinterpret_cast<uint32_t*>(smem + L::kBars + 16);
+  if (warp == 0) tc::tmem_alloc(tc::smem_u32(smem + L::kBars + 16), L::kColumns);
+  if (tid == 32) {
+    tc::mbar_init(done, 1);
+    tc::mbar_init(done + 8, 1);
+    tc::fence_mbar_init();
+    slot[1] = 0;
+  }
+  if (tid >= 64) {
+    const int i = tid - 64;
+    const int m = i < x.count ? p.plan[x.first + i] : 0;
+    const bool ok = SEEDLM_IN_BOUNDS(g_check_flag, m, p.M);
+    from_row[i] = ok ? m * p.ldb + p.slice_at[x.s] : p.slice_at[x.s];
+    to_row[i] = ok ? m * p.ldy + p.slice_at[x.s] : p.slice_at[x.s];
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  // Only now: a kernel after this one that takes all tensor memory and then
+  // waits for this one must not come before this one has its own.
+  grid_launch_dependents();
+  const uint32_t tmem = slot[0];
+
+  // This thread's units of B: 16 bytes `unit` of rows row0, row0 + 16, ...
   const uint16_t* B = static_cast<const uint16_t*>(p.ad.B[x.s]) + max(x.a, 0) * p.ad.b_adapter[x.s];
   const int64_t b_row = p.ad.b_row[x.s];
-  const bool vec_b = (p.vec_b >> x.s) & 1, vec_y = (p.vec_y >> x.s) & 1;
-  if (threadIdx.x < T) {
-    const int m = threadIdx.x < x.count ? p.plan[x.first + threadIdx.x] : -1;
-    const bool ok = m >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, m, p.M);
-    from_row[threadIdx.x] = ok ? m * p.ldb + p.slice_at[x.s] : -1;
-    to_row[threadIdx.x] = ok ? m * p.ldy + p.slice_at[x.s] : -1;
-  }
-  __syncthreads();
-  const bool full = x.count == T;
-  auto fetch = [&](int n0) {
-    if (vec_y && n0 + 32 <= x.c1) {
-      const float* base = p.base + n0 + 4 * g;
+  const bool vec_b = (p.vec_b >> x.s) & 1;
+  const int unit = tid % 8, row0 = tid / 8;
+  const int place = row0 * 128 + (unit ^ (row0 & 7)) * 16;
+  const int tiles = (x.c1 - x.c0 + kOut - 1) / kOut;
+  auto fetch = [&](int i) {
+    if (i < tiles) {
+      unsigned char* stage = smem + L::kB + i % kSt * L::kStageBytes + place;
+      const int n = x.c0 + i * kOut + row0;
+      const uint16_t* src = B + n * b_row + 8 * unit;
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+      for (int b = 0; b < NB; ++b) {
+        const int left = x.rank - 64 * b - 8 * unit;
+        if (vec_b) {
+          const int bytes = max(0, min(16, 2 * left));
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int64_t row = from_row[8 * i + 2 * q + e];
-          copy16(ring + (2 * i + e) * 512, base + max(row, (int64_t)0), row >= 0 ? 16 : 0);
+          for (int j = 0; j < kOut / 16; ++j)
+            copy16_short(stage + b * kOut * 128 + j * 16 * 128, src + 64 * b + j * 16 * b_row,
+                         n + 16 * j < x.c1 ? bytes : 0);
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < kOut / 16; ++j)
+            *reinterpret_cast<uint4*>(stage + b * kOut * 128 + j * 16 * 128) =
+                load8_slow(src + 64 * b + j * 16 * b_row, 0, n + 16 * j < x.c1 ? left : 0);
         }
+      }
     }
     copies_commit();
   };
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  uint4 w[4], ahead[4];
-  const bool units = vec_b && x.rank % 8 == 0;
-  auto load_b = [&](int n0, int r) {
-    const uint16_t* b = B + (n0 + 4 * g) * b_row + r;
-    if (units && n0 + 32 <= x.c1) {
-      if (r < x.rank) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) ahead[j] = __ldg(reinterpret_cast<const uint4*>(b + j * b_row));
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) ahead[j] = zero;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) ahead[j] = load8_slow(b + j * b_row, 0, n0 + 4 * g + j < x.c1 ? x.rank - r : 0);
-    }
-  };
-  int n0 = x.c0 + 32 * warp;
-  load_b(n0, 8 * q);
+#pragma unroll 1
+  for (int i = 0; i < kSt; ++i) fetch(i);
   grid_wait();
-  // The tile's S: units of 8 ranks; what lies beyond the last whole step of 32
-  // is not read below.
-  constexpr int kUnits = kStride / 8;
-  const int rank_units = (x.rank + kStep - 1) / kStep * (kStep / 8);
-  for (int u = threadIdx.x; u < P * T * kUnits; u += kThreads) {
-    const int r = u % kUnits, i = u / kUnits % T, pt = u / (kUnits * T);
-    if (r >= rank_units) continue;
-    const uint16_t* src = p.S + (((int64_t)(x.first + (i < x.count ? i : 0)) * p.ad.slices + x.s) * P + pt) * p.slots + 8 * r;
-    const int to = (pt * T + i) * kStride + 8 * (RC % 2 ? r : r ^ (i & 1) * 4);
-    copy16(sp + to, src, i < x.count ? 16 : 0);
+#pragma unroll
+  for (int j = 0; j < T / 16; ++j) {
+    const int i = row0 + 16 * j;
+    const uint16_t* src = p.S + ((int64_t)(x.first + (i < x.count ? i : 0)) * p.ad.slices + x.s) * P * p.slots + 8 * unit;
+#pragma unroll
+    for (int pt = 0; pt < P; ++pt)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        copy16(smem + (pt * NB + b) * T * 128 + j * 16 * 128 + place, src + pt * p.slots + 64 * b,
+               i < x.count && 64 * b + 8 * unit < p.slots && 64 * b < x.rank ? 16 : 0);
   }
+  float* unscale = reinterpret_cast<float*>(smem + L::kScales);
   if constexpr (!BF16)
-    for (int u = threadIdx.x; u < T * kBlocks; u += kThreads) {
-      const int i = u / kBlocks, b = u % kBlocks;
+    for (int u = tid; u < NB * T; u += L::kThreads) {
+      const int i = u % T, b = u / T;
       unscale[u] = i < x.count && 64 * b < x.rank
                        ? __ldcg(p.unscale + ((int64_t)(x.first + i) * p.ad.slices + x.s) * p.blocks + b)
                        : 0.f;
     }
   copies_commit();
-  fetch(n0);
-  copies_wait<1>();
-  __syncthreads();
-  const uint16_t* srow = sp + g * kStride;
-  const int swap = RC % 2 ? 0 : (g & 1) * kStep;
-  for (; n0 < x.c1; n0 += kRound) {
-    float acc[2][NT][4] = {};
-    float total[BF16 || kBlocks == 1 ? 1 : 2][NT][4] = {};  // fp16: the blocks before this one, where there are many
-#pragma unroll 1
-    for (int k = 0; k < x.rank; k += kStep) {
+
+  // The products of tile i, by the first warp.
+  auto multiply = [&](int i) {
+    const uint32_t idesc = tc::idesc_f16(T, BF16 ? 1 : 0);
+    const uint64_t w = tc::smem_desc_sw128(tc::smem_u32(smem + L::kB + i % kSt * L::kStageBytes));
+    const uint64_t v = tc::smem_desc_sw128(tc::smem_u32(smem));
+    uint32_t more = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = ahead[j];
-      const bool more = k + kStep < x.rank;
-      load_b(more ? n0 : n0 + kRound, (more ? k + kStep : 0) + 8 * q);
-      const uint16_t* from = srow + ((k + 8 * q) ^ swap);
+    for (int b = 0; b < NB; ++b) {
+      const uint32_t d = tmem + (i & 1) * L::kSums * T + (BF16 ? 0 : b * T);
+      const int steps = min(4, (x.rank - 64 * b + 15) / 16);
+      if (!BF16) more = 0;
+      // The smallest parts first.
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int pt = 0; pt < P; ++pt) {
-          const uint4 v = *reinterpret_cast<const uint4*>(from + (pt * T + 8 * i) * kStride);
-          mma_step<BF16>(acc[0][i], w[0], w[1], v);
-          mma_step<BF16>(acc[1][i], w[2], w[3], v);
+      for (int pt = P - 1; pt >= 0; --pt)
+        for (int k = 0; k < steps; ++k) {
+          tc::mma_f16_ss_warp(d, w + (uint64_t)(b * kOut * 128 / 16 + 2 * k),
+                              v + (uint64_t)((pt * NB + b) * T * 128 / 16 + 2 * k), idesc, more);
+          more = 1;
         }
-      if constexpr (!BF16 && kBlocks > 1) {
-        if (!more || k % 64 != 0)
-#pragma unroll
-          for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float f = unscale[(8 * i + 2 * q + e % 2) * kBlocks + k / 64];
-#pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                total[b][i][e] = fmaf(acc[b][i][e], f, total[b][i][e]);
-                acc[b][i][e] = 0.f;
-              }
-            }
-      }
     }
-    if constexpr (!BF16) {
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if constexpr (kBlocks > 1) acc[b][i][e] = total[b][i][e];
-            else acc[b][i][e] *= unscale[8 * i + 2 * q + e % 2];
-          }
-    }
+    tc::mma_commit_warp(done + 8 * (i & 1));
+  };
+  const bool products = x.rank > 0;
+  if (products) {
     copies_wait<0>();
-    const bool whole = vec_y && n0 + 32 <= x.c1;
-    float* out = p.Y + n0 + 4 * g;
-    if (whole && full) {
+    tc::fence_proxy_async();
+    __syncthreads();
+    if (warp == 0) multiply(0);
+  }
+  bool ok = true;
+  for (int i = 0; i < tiles; ++i) {
+    const int n = x.c0 + i * kOut + tid;
+    float v[T];
+    const float* from = p.base + n;
+    const bool full = x.count == T && x.c0 + (i + 1) * kOut <= x.c1;
+    if (full) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float4 b = *reinterpret_cast<const float4*>(ring + (2 * i + e) * 512);
-          *reinterpret_cast<float4*>(out + to_row[8 * i + 2 * q + e]) =
-              make_float4(b.x + acc[0][i][e], b.y + acc[0][i][2 + e], b.z + acc[1][i][e], b.w + acc[1][i][2 + e]);
-        }
+      for (int r = 0; r < T; ++r) v[r] = __ldcg(from + from_row[r]);
     } else {
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+      for (int r = 0; r < T; ++r) v[r] = r < x.count && n < x.c1 ? __ldcg(from + from_row[r]) : 0.f;
+    }
+    if (products) {
+      if (i + 1 < tiles) {
+        copies_wait<kSt - 2>();
+        tc::fence_proxy_async();
+        tc::fence_before_sync();  // of the sums of tile i - 1, read
+        __syncthreads();
+        tc::fence_after_sync();
+        if (warp == 0) multiply(i + 1);
+      }
+      ok = tc::mbar_wait_or_abort(done + 8 * (i & 1), (i >> 1) & 1, kTallWaitLimit, slot + 1) && ok;
+      tc::fence_after_sync();
+      fetch(i + kSt);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int row = 8 * i + 2 * q + e;
-          const int64_t to = to_row[row];
-          if (to < 0) continue;
-          const float4 d = make_float4(acc[0][i][e], acc[0][i][2 + e], acc[1][i][e], acc[1][i][2 + e]);
-          if (whole) {
-            const float4 b = *reinterpret_cast<const float4*>(ring + (2 * i + e) * 512);
-            *reinterpret_cast<float4*>(out + to) = make_float4(b.x + d.x, b.y + d.y, b.z + d.z, b.w + d.w);
-          } else {
-            add4_slow(out + to, p.base + n0 + 4 * g + from_row[row], d, x.c1 - n0 - 4 * g);
-          }
+      for (int c = 0; c < T / 16; ++c)
+#pragma unroll
+        for (int b = 0; b < L::kSums; ++b) {
+          float d[16];
+          tc::tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + (i & 1) * L::kSums * T + b * T + 16 * c, d);
+          if (BF16 || 64 * b < x.rank)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              if constexpr (BF16) v[16 * c + r] += d[r];
+              else v[16 * c + r] = fmaf(d[r], unscale[b * T + 16 * c + r], v[16 * c + r]);
+            }
         }
     }
-    fetch(n0 + kRound);
+    float* to = p.Y + n;
+    if (!ok) continue;
+    if (full) {
+#pragma unroll
+      for (int r = 0; r < T; ++r) to[to_row[r]] = v[r];
+    } else {
+#pragma unroll
+      for (int r = 0; r < T; ++r)
+        if (r < x.count && n < x.c1) to[to_row[r]] = v[r];
+    }
+  }
+  if (!ok && lane == 0) atomicOr(&g_wait_error, 1u);
+  copies_wait<0>();
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, L::kColumns);
   }
 }
 
@@ -1044,10 +1120,11 @@ int launch_expand_low(const ApplyArgs& p, int64_t grid, int chunks, cudaStream_t
                                 stream, dev, p, chunks, (int)(p.base == p.Y));
 }
 
-template <bool BF16, int RC>
+template <bool BF16, int NB>
 int launch_expand_tall(const ApplyArgs& p, int64_t grid, int chunks, cudaStream_t stream, const DeviceInfo& dev) {
-  return launch_products_kernel(adapters_expand_tall_kernel<BF16, RC>, grid, kThreads, kExpandTallSmem<BF16, RC>, 1,
-                                stream, dev, p, chunks, (int)(p.base == p.Y));
+  using L = TallLayout<BF16, NB>;
+  return launch_products_kernel(adapters_expand_tall_kernel<BF16, NB>, grid, L::kThreads, L::kBytes, 1, stream, dev, p,
+                                chunks, (int)(p.base == p.Y));
 }
 
 template <bool BF16>
@@ -1067,7 +1144,7 @@ int launch_products(ApplyArgs& p, const ShrinkShape& sh, int64_t tiles, cudaStre
   // CTA's warps.
   int64_t total = 0;
   for (int s = 0; s < p.ad.slices; ++s) total += p.ad.rows[s];
-  const int round = 32 * (low ? kLowWarps : kWarps);
+  const int round = 128;  // outputs: of four warps, or of one product
   int64_t rounds = total * tiles / ((int64_t)round * (low ? 12 : 8) * dev.num_sms);
   rounds = rounds < 1 ? 1 : rounds > 16 ? 16 : rounds;
   p.chunk_rows = (int)rounds * round;
@@ -1086,10 +1163,9 @@ int launch_products(ApplyArgs& p, const ShrinkShape& sh, int64_t tiles, cudaStre
     return p.slots == 32   ? launch_expand_low<BF16, 1, false>(p, grid, (int)chunks, stream, dev)
            : p.slots == 64 ? launch_expand_low<BF16, 2, false>(p, grid, (int)chunks, stream, dev)
                            : launch_expand_low<BF16, 2, true>(p, grid, (int)chunks, stream, dev);
-  return p.slots == 32    ? launch_expand_tall<BF16, 1>(p, grid, (int)chunks, stream, dev)
-         : p.slots == 64  ? launch_expand_tall<BF16, 2>(p, grid, (int)chunks, stream, dev)
-         : p.slots == 128 ? launch_expand_tall<BF16, 4>(p, grid, (int)chunks, stream, dev)
-                          : launch_expand_tall<BF16, 8>(p, grid, (int)chunks, stream, dev);
+  return p.blocks == 1   ? launch_expand_tall<BF16, 1>(p, grid, (int)chunks, stream, dev)
+         : p.blocks == 2 ? launch_expand_tall<BF16, 2>(p, grid, (int)chunks, stream, dev)
+                         : launch_expand_tall<BF16, 4>(p, grid, (int)chunks, stream, dev);
 }
 
 // Bytes of S, then those of its factors.
@@ -1144,6 +1220,14 @@ int read_and_clear_plan_mismatch(unsigned int* out) {
   unsigned int v = 0, zero = 0;
   cudaError_t err = cudaMemcpyFromSymbol(&v, g_plan_mismatch, sizeof(v));
   if (err == cudaSuccess && v) err = cudaMemcpyToSymbol(g_plan_mismatch, &zero, sizeof(zero));
+  *out = v;
+  return record_cuda_error(err);
+}
+
+int read_and_clear_adapters_error(unsigned int* out) {
+  unsigned int v = 0, zero = 0;
+  cudaError_t err = cudaMemcpyFromSymbol(&v, g_wait_error, sizeof(v));
+  if (err == cudaSuccess && v) err = cudaMemcpyToSymbol(g_wait_error, &zero, sizeof(zero));
   *out = v;
   return record_cuda_error(err);
 }

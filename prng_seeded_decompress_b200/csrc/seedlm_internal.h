@@ -143,6 +143,7 @@ int launch_adapters_apply(const seedlm_adapters& ad, const int32_t* plan, int M,
                           int64_t ldx, const float* base, int64_t ldb, float* Y, int64_t ldy,
                           void* workspace, cudaStream_t stream, const DeviceInfo& dev);
 int read_and_clear_plan_mismatch(unsigned int* out);
+int read_and_clear_adapters_error(unsigned int* out);
 // Block boundary and gated activation (block_norm.cu).
 int launch_block_norm(const seedlm_norm& nm, int M, const float* y, int64_t ldy, const void* gate,
                       int64_t ldg, const void* h, int64_t ldh, void* h_out, int64_t ldho,

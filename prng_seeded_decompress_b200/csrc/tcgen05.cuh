@@ -28,6 +28,21 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
   return d;
 }
 
+// Shared-memory matrix descriptor, K-major operand in the 128-byte swizzle: rows
+// of 128 bytes (64 16-bit elements), the 16-byte unit u of row r at place
+// u ^ (r % 8), groups of 8 rows 1024 bytes apart from a 1024-byte boundary.
+// Step k of 16 elements starts 32 k bytes further (add 2 k to the descriptor).
+// Fields as above, layout type 2.
+__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)1 << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
 // Instruction descriptor for kind::f16: D fp32, A and B both fp16 (bf16 = 0)
 // or both bf16 (bf16 = 1), K-major, M = 128, N = n (multiple of 16, <= 256).
 __host__ __device__ constexpr uint32_t idesc_f16(int n, int bf16) {
@@ -54,6 +69,23 @@ __device__ __forceinline__ void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem
       :
       : "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(0u), "r"(0u),
         "r"(0u), "r"(0u));
+}
+// The same with A in shared memory as well.
+__device__ __forceinline__ void mma_f16_ss_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}\n"
+      :
+      : "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(0u), "r"(0u),
+        "r"(0u), "r"(0u));
+}
+// Writes to shared memory by this thread (asynchronous copies it has waited
+// for among them) become visible to the tensor cores' reads.
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 // Eight K = 16 steps of two pieces (16 MMAs) in one statement: piece pc of
 // step k reads A at a0 + pc * pcols + 8 k and B at b_desc + 16 k (the
