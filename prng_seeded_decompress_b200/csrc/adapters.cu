@@ -41,59 +41,120 @@ inline int64_t max_tiles(int64_t M, int64_t n) {
   return M / adapter_tile_rows((int)M) + (M < n + 1 ? M : n + 1);
 }
 
-constexpr int kPlanMaxThreads = 1024;
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// All threads of all CTAs of the cluster; shared memory written before is
+// visible after.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
 
-// A stable counting sort by one CTA.  Each warp takes one contiguous part of
-// the rows and counts its adapters in a histogram of its own (match_any
-// groups the lanes of a step, so no two lanes touch a bin); the histograms
-// are turned into starting places bin by bin, and a second walk over the same
-// rows puts each at its place.  Latency bound: two passes over 4 M bytes and
-// four barriers.
-__global__ void __launch_bounds__(kPlanMaxThreads, 1)
+// A stable counting sort by one cluster: one CTA, or eight for many rows.  Each
+// warp takes one contiguous part of the rows and counts its adapters in a
+// histogram of its own (match_any groups the lanes of a step, so no two lanes
+// touch a bin).  Bin by bin the histograms become starting places: over the
+// warps of a CTA, then over the CTAs through distributed shared memory, then
+// over the bins.  A second walk over the same rows puts each at its place.
+// Latency bound: a few dependent steps, so each lane has 16 of its rows' ids in
+// flight at once and keeps them for the second walk where they are all it has.
+constexpr int kPlanThreads = 1024, kPlanCtas = 8;
+constexpr int kPlanSteps = 16;  // ids a lane holds
+constexpr int kPlanOneCtaRows = 2048;
+
+__device__ __forceinline__ int load_of_cta(const int* mine, uint32_t cta) {
+  uint32_t at;
+  int v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(cta));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1)
 adapters_plan_kernel(int M, int n, int T, const int32_t* __restrict__ ids, int32_t* __restrict__ plan,
                      int64_t tail_words) {
   extern __shared__ int32_t sm[];
   const int bins = n + 1, nwarps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  int32_t* hist = sm;                            // [nwarps][bins]
-  int32_t* start = hist + (size_t)nwarps * bins; // [bins + 1]
-  int32_t* tstart = start + bins + 1;            // [bins + 1]
-  int32_t* warp_rows = tstart + bins + 1;        // [nwarps]
-  int32_t* warp_tiles = warp_rows + nwarps;      // [nwarps]
+  const int cta = (int)cluster_rank(), ctas = (int)cluster_size();
+  int32_t* hist = sm;                             // [nwarps][bins]
+  int32_t* total = hist + (size_t)nwarps * bins;  // [bins] rows of each bin in this CTA
+  int32_t* base = total + bins;                   // [bins] place of this CTA's first row of each bin
+  int32_t* start = base + bins;                   // [bins + 1] of all CTAs
+  int32_t* tstart = start + bins + 1;             // [bins + 1] tiles before each bin
+  int32_t* warp_rows = tstart + bins + 1;         // [nwarps]
+  int32_t* warp_tiles = warp_rows + nwarps;       // [nwarps]
   grid_launch_dependents();
   for (int i = threadIdx.x; i < nwarps * bins; i += blockDim.x) hist[i] = 0;
   grid_wait();
   __syncthreads();
-  const int chunk = ((M + nwarps - 1) / nwarps + 31) / 32 * 32;
-  const int r0 = min(M, warp * chunk), r1 = min(M, r0 + chunk);
+  const int chunk = ((M + ctas * nwarps - 1) / (ctas * nwarps) + 31) / 32 * 32;
+  const int64_t first = (int64_t)(cta * nwarps + warp) * chunk;
+  const int r0 = (int)(first < M ? first : M), r1 = min(M, r0 + chunk);
   int32_t* mine = hist + (size_t)warp * bins;
-  for (int r = r0; r < r1; r += 32) {
-    const int row = r + lane;
-    int key = -1;
-    if (row < r1) {
-      const int id = ids[row];
-      key = id >= 0 && id < n ? id : n;
+  int key[kPlanSteps];  // of row r + 32 i + lane: its bin, -1 for no row
+  auto load = [&](int r) {
+#pragma unroll
+    for (int i = 0; i < kPlanSteps; ++i) {
+      const int row = r + 32 * i + lane;
+      key[i] = row < r1 ? ids[row] : 0;
     }
-    const unsigned same = __match_any_sync(0xffffffffu, key);
-    if (key >= 0 && (same & ((1u << lane) - 1)) == 0) mine[key] += __popc(same);
-    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kPlanSteps; ++i) {
+      if (key[i] < 0 || key[i] >= n) key[i] = n;
+      if (r + 32 * i + lane >= r1) key[i] = -1;
+    }
+  };
+  for (int r = r0; r < r1; r += 32 * kPlanSteps) {
+    load(r);
+#pragma unroll
+    for (int i = 0; i < kPlanSteps; ++i) {
+      if (r + 32 * i >= r1) break;
+      const unsigned same = __match_any_sync(0xffffffffu, key[i]);
+      if (key[i] >= 0 && (same & ((1u << lane) - 1)) == 0) mine[key[i]] += __popc(same);
+      __syncwarp();
+    }
   }
   __syncthreads();
-  // Exclusive sums over the warps of each bin; then over the bins, each
-  // thread taking `per` consecutive ones.
-  const int per = (bins + blockDim.x - 1) / blockDim.x;
-  const int b0 = min(bins, (int)threadIdx.x * per), b1 = min(bins, b0 + per);
-  int rows = 0, tiles = 0;
-  for (int b = b0; b < b1; ++b) {
+  for (int b = threadIdx.x; b < bins; b += blockDim.x) {
     int run = 0;
+#pragma unroll 8
     for (int w = 0; w < nwarps; ++w) {
       const int t = hist[w * bins + b];
       hist[w * bins + b] = run;
       run += t;
     }
+    total[b] = run;
+  }
+  if (ctas > 1) cluster_sync();
+  else __syncthreads();
+  // Every CTA scans all bins, each thread taking `per` consecutive ones.
+  const int per = (bins + blockDim.x - 1) / blockDim.x;
+  const int b0 = min(bins, (int)threadIdx.x * per), b1 = min(bins, b0 + per);
+  int rows = 0, tiles = 0;
+  for (int b = b0; b < b1; ++b) {
+    int before = 0, all = 0;
+    if (ctas == 1) {
+      all = total[b];
+    } else {
+#pragma unroll
+      for (int c = 0; c < kPlanCtas; ++c) {
+        const int v = load_of_cta(total + b, c);
+        all += v;
+        if (c < cta) before += v;
+      }
+    }
     start[b] = rows;  // within this thread's bins
     tstart[b] = tiles;
-    rows += run;
-    tiles += (run + T - 1) / T;
+    base[b] = before;
+    rows += all;
+    tiles += (all + T - 1) / T;
   }
   int2 incl = make_int2(rows, tiles);
 #pragma unroll
@@ -106,50 +167,56 @@ adapters_plan_kernel(int M, int n, int T, const int32_t* __restrict__ ids, int32
     warp_tiles[warp] = incl.y;
   }
   __syncthreads();
-  int2 before = make_int2(incl.x - rows, incl.y - tiles);
-  for (int w = 0; w < warp; ++w) before = make_int2(before.x + warp_rows[w], before.y + warp_tiles[w]);
+  // Sums of the warps before this one, a lane each.
+  int2 before = make_int2(lane < warp ? warp_rows[lane] : 0, lane < warp ? warp_tiles[lane] : 0);
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2)
+    before = make_int2(before.x + __shfl_xor_sync(0xffffffffu, before.x, o),
+                       before.y + __shfl_xor_sync(0xffffffffu, before.y, o));
+  before = make_int2(before.x + incl.x - rows, before.y + incl.y - tiles);
   for (int b = b0; b < b1; ++b) {
     start[b] += before.x;
     tstart[b] += before.y;
-    plan[M + b] = start[b];
+    base[b] += start[b];
+    if (cta == 0) plan[M + b] = start[b];
   }
   if (b1 == bins && b0 < bins) {  // the thread of the last bin
     start[bins] = before.x + rows;
     tstart[bins] = before.y + tiles;
   }
   __syncthreads();
-  for (int r = r0; r < r1; r += 32) {
-    const int row = r + lane;
-    int key = -1;
-    if (row < r1) {
-      const int id = ids[row];
-      key = id >= 0 && id < n ? id : n;
+  for (int r = r0; r < r1; r += 32 * kPlanSteps) {
+    if (chunk > 32 * kPlanSteps) load(r);
+#pragma unroll
+    for (int i = 0; i < kPlanSteps; ++i) {
+      if (r + 32 * i >= r1) break;
+      const unsigned same = __match_any_sync(0xffffffffu, key[i]);
+      const int rank = __popc(same & ((1u << lane) - 1));
+      int at = 0;
+      if (key[i] >= 0) at = base[key[i]] + mine[key[i]] + rank;
+      __syncwarp();
+      if (key[i] >= 0) {
+        if (SEEDLM_IN_BOUNDS(g_check_flag, at, M)) plan[at] = r + 32 * i + lane;
+        if (rank == 0) mine[key[i]] += __popc(same);
+      }
+      __syncwarp();
     }
-    const unsigned same = __match_any_sync(0xffffffffu, key);
-    const int rank = __popc(same & ((1u << lane) - 1));
-    int at = 0;
-    if (key >= 0) at = start[key] + mine[key] + rank;
-    __syncwarp();
-    if (key >= 0) {
-      if (SEEDLM_IN_BOUNDS(g_check_flag, at, M)) plan[at] = row;
-      if (rank == 0) mine[key] += __popc(same);
-    }
-    __syncwarp();
   }
   int32_t* tail = plan + plan_tail(M, n);
-  const int total = tstart[bins];
-  if (threadIdx.x == 0) *reinterpret_cast<int4*>(tail) = make_int4(M, n, tstart[n], total);
-  for (int t = threadIdx.x; t < total; t += blockDim.x) {
+  const int all = tstart[bins];
+  if (cta == 0 && threadIdx.x == 0) *reinterpret_cast<int4*>(tail) = make_int4(M, n, tstart[n], all);
+  for (int t = cta * blockDim.x + threadIdx.x; t < all; t += ctas * blockDim.x) {
     int lo = 0, hi = bins - 1;  // the last bin that starts at or before tile t
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
       if (tstart[mid] <= t) lo = mid;
       else hi = mid - 1;
     }
-    const int first = start[lo] + (t - tstart[lo]) * T;
+    const int at = start[lo] + (t - tstart[lo]) * T;
     if (SEEDLM_IN_BOUNDS(g_check_flag, 4 + 4 * (int64_t)t + 3, tail_words))
-      reinterpret_cast<int4*>(tail)[1 + t] = make_int4(lo < n ? lo : -1, first, min(T, start[lo + 1] - first), 0);
+      reinterpret_cast<int4*>(tail)[1 + t] = make_int4(lo < n ? lo : -1, at, min(T, start[lo + 1] - at), 0);
   }
+  if (ctas > 1) cluster_sync();  // no CTA leaves while another reads its totals
 }
 
 // ------------------------------------------------------------- the products
@@ -271,21 +338,6 @@ __device__ __forceinline__ void copies_wait() {
 
 // ---- the first kernel's end: the cluster's sums to S
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-// All threads of all CTAs of the cluster; shared memory written before is
-// visible after.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
 __device__ __forceinline__ float2 load_of_cta(const float* mine, uint32_t cta) {
   uint32_t at;
   float2 v;
@@ -1050,12 +1102,15 @@ int64_t adapters_plan_words(int M, int n) { return plan_tail(M, n) + 4 + 4 * max
 int launch_adapters_plan(int M, int n, const int32_t* ids, int32_t* plan, cudaStream_t stream, const DeviceInfo& dev) {
   int rc = allow_max_smem((const void*)adapters_plan_kernel, dev);
   if (rc) return rc;
+  // One CTA up to 2048 rows; the cluster's two barriers cost more there than
+  // its eight times as many threads save.
+  const int ctas = M > kPlanOneCtaRows ? kPlanCtas : 1;
   const int most = M > n + 1 ? M : n + 1;
-  const int threads = most >= kPlanMaxThreads ? kPlanMaxThreads : (most + 31) / 32 * 32;
+  const int threads = most >= kPlanThreads ? kPlanThreads : (most + 31) / 32 * 32;
   const int nwarps = threads / 32, bins = n + 1;
-  const size_t smem = ((size_t)nwarps * bins + 2 * (bins + 1) + 2 * nwarps) * sizeof(int32_t);
-  return launch_pdl(adapters_plan_kernel, 1, threads, smem, stream, M, n, adapter_tile_rows(M), ids, plan,
-                    adapters_plan_words(M, n) - plan_tail(M, n));
+  const size_t smem = ((size_t)nwarps * bins + 4 * bins + 2 + 2 * nwarps) * sizeof(int32_t);
+  return launch_pdl_cluster(adapters_plan_kernel, ctas, threads, smem, ctas, stream, M, n, adapter_tile_rows(M), ids,
+                            plan, adapters_plan_words(M, n) - plan_tail(M, n));
 }
 
 namespace {

@@ -26,16 +26,33 @@ __device__ __forceinline__ void store_as(void* p, int64_t i, int dtype, float v)
   else static_cast<__half*>(p)[i] = __float2half_rn(v);
 }
 
-// Sum over the CTA, in a fixed order, to every thread.
-__device__ float block_sum(float v, float* red) {
+__device__ __forceinline__ float2 two_of(uint32_t w, bool bf16) {
+  return bf16 ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u))
+              : __half22float2(reinterpret_cast<const __half2&>(w));
+}
+
+__device__ __forceinline__ uint32_t two_to(float a, float b, bool bf16) {
+  if (bf16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return reinterpret_cast<const uint32_t&>(v);
+  }
+  const __half2 v = __floats2half2_rn(a, b);
+  return reinterpret_cast<const uint32_t&>(v);
+}
+
+// Sum over the CTA to every thread, in a fixed order; `red` holds a float for
+// each warp and is used by one sum at a time.
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
 #pragma unroll
   for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (warps == 1) return v;
+  if (lane == 0) red[warp] = v;
   __syncthreads();
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
-  __syncthreads();
-  float s = 0.f;
-  for (int w = 0; w < (int)blockDim.x / 32; ++w) s += red[w];
-  return s;
+  v = lane < warps ? red[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
 struct NormArgs {
@@ -54,6 +71,203 @@ struct NormArgs {
   int x_dtype;
 };
 
+// A thread's share of a row: NV groups of four elements, neighbouring ones
+// (VEC) or, where rows are not aligned for that, ones a CTA's width apart.  The
+// type is looked at once for a share, so that all its loads are in flight
+// together.
+template <int NV, bool VEC>
+struct Share {
+  __device__ static int index(int i, int k) {
+    return VEC ? 4 * ((int)threadIdx.x + (int)blockDim.x * i) + k : (int)threadIdx.x + (int)blockDim.x * (4 * i + k);
+  }
+  // 16-bit elements as they are stored; zeros beyond the row.
+  __device__ static void load16(const void* p, int64_t row, int cols, uint2 (&raw)[NV]) {
+    const uint16_t* from = static_cast<const uint16_t*>(p) + row;
+    if (VEC) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        raw[i] = index(i, 0) < cols ? *reinterpret_cast<const uint2*>(from + index(i, 0)) : make_uint2(0u, 0u);
+    } else {
+      uint16_t e[NV][4];
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) e[i][k] = index(i, k) < cols ? from[index(i, k)] : (uint16_t)0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        raw[i] = make_uint2(e[i][0] | (uint32_t)e[i][1] << 16, e[i][2] | (uint32_t)e[i][3] << 16);
+    }
+  }
+  __device__ static void load32(const void* p, int64_t row, int cols, float (&v)[NV][4]) {
+    const float* from = static_cast<const float*>(p) + row;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (VEC) {
+        const float4 a = index(i, 0) < cols ? *reinterpret_cast<const float4*>(from + index(i, 0)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[i][k] = index(i, k) < cols ? from[index(i, k)] : 0.f;
+      }
+    }
+  }
+  __device__ static void widen(const uint2 (&raw)[NV], bool bf16, float (&v)[NV][4]) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float2 lo = two_of(raw[i].x, bf16), hi = two_of(raw[i].y, bf16);
+      v[i][0] = lo.x, v[i][1] = lo.y, v[i][2] = hi.x, v[i][3] = hi.y;
+    }
+  }
+  __device__ static void store(void* p, int64_t row, int cols, int dtype, const float (&v)[NV][4]) {
+    if (dtype == SEEDLM_F32) {
+      float* to = static_cast<float*>(p) + row;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (VEC) {
+          if (index(i, 0) < cols)
+            *reinterpret_cast<float4*>(to + index(i, 0)) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (index(i, k) < cols) to[index(i, k)] = v[i][k];
+        }
+    } else {
+      uint16_t* to = static_cast<uint16_t*>(p) + row;
+      const bool bf16 = dtype == SEEDLM_BF16;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const uint2 a = make_uint2(two_to(v[i][0], v[i][1], bf16), two_to(v[i][2], v[i][3], bf16));
+        if (VEC) {
+          if (index(i, 0) < cols) *reinterpret_cast<uint2*>(to + index(i, 0)) = a;
+        } else {
+          const uint32_t w[2] = {a.x, a.y};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (index(i, k) < cols) to[index(i, k)] = (uint16_t)(w[k / 2] >> (16 * (k % 2)));
+        }
+      }
+    }
+  }
+};
+
+// A share of some type, asked for early and used late: 16-bit elements wait in
+// registers as they are; fp32 ones would take too many and are loaded when used.
+template <int NV, bool VEC>
+struct Early {
+  uint2 raw[NV];
+  __device__ void ask(const void* p, int64_t row, int cols, int dtype) {
+    if (p && dtype != SEEDLM_F32) Share<NV, VEC>::load16(p, row, cols, raw);
+  }
+  __device__ void use(const void* p, int64_t row, int cols, int dtype, float (&v)[NV][4]) const {
+    if (dtype != SEEDLM_F32) Share<NV, VEC>::widen(raw, dtype == SEEDLM_BF16, v);
+    else Share<NV, VEC>::load32(p, row, cols, v);
+  }
+};
+
+// v <- norm(v), all but weights and bias; two passes over registers.
+template <int NV, bool VEC>
+__device__ __forceinline__ void normalise(float (&v)[NV][4], const seedlm_norm& nm, float* red) {
+  const float inv = 1.f / nm.cols;
+  if (nm.kind == SEEDLM_NORM_LAYER) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s += (v[i][0] + v[i][1]) + (v[i][2] + v[i][3]);
+    const float mean = block_sum(s, red) * inv;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[i][k] = Share<NV, VEC>::index(i, k) < nm.cols ? v[i][k] - mean : 0.f;
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    s += fmaf(v[i][0], v[i][0], v[i][1] * v[i][1]) + fmaf(v[i][2], v[i][2], v[i][3] * v[i][3]);
+  const float rstd = rsqrtf(block_sum(s, red + 32) * inv + nm.eps);
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[i][k] *= rstd;
+}
+
+template <int NV, bool VEC>
+__device__ __forceinline__ void weigh(float (&v)[NV][4], const seedlm_norm& nm, const void* w, const void* b,
+                                      const Early<NV, VEC>& early_w) {
+  float t[NV][4];
+  if (w) {
+    early_w.use(w, 0, nm.cols, nm.dtype, t);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[i][k] *= nm.weight_offset + t[i][k];
+  }
+  if (b) {
+    Early<NV, VEC> late;
+    late.ask(b, 0, nm.cols, nm.dtype);
+    late.use(b, 0, nm.cols, nm.dtype, t);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[i][k] += t[i][k];
+  }
+}
+
+// One CTA a row, which stays in registers: y and h are read once, h' and x
+// written once.
+template <int NV>
+constexpr int kRowThreads = NV == 8 ? 512 : 1024;
+
+template <int NV, bool VEC>
+__global__ void __launch_bounds__(kRowThreads<NV>) block_norm_kernel(const __grid_constant__ NormArgs p) {
+  __shared__ float red[4][32];  // one place for each sum of a row
+  const seedlm_norm& nm = p.nm;
+  const int cols = nm.cols;
+  const int64_t m = blockIdx.x;
+  using S = Share<NV, VEC>;
+  grid_launch_dependents();
+  grid_wait();
+  float v[NV][4], h[NV][4];
+  Early<NV, VEC> w, stream, gate;
+  if (p.y) {
+    S::load32(p.y, m * p.ldy, cols, v);
+    gate.ask(p.gate, m * p.ldg, cols, nm.dtype);
+    if (nm.post) w.ask(nm.w_post, 0, cols, nm.dtype);
+  }
+  stream.ask(p.h, m * p.ldh, cols, p.h_dtype);
+  if (p.y) {
+    if (nm.post) {
+      normalise<NV, VEC>(v, nm, red[0]);
+      weigh<NV, VEC>(v, nm, nm.w_post, nm.b_post, w);
+    }
+    if (p.gate) {
+      gate.use(p.gate, m * p.ldg, cols, nm.dtype, h);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[i][k] *= h[i][k];
+    }
+  }
+  if (p.h) stream.use(p.h, m * p.ldh, cols, p.h_dtype, h);
+  if (p.x && nm.pre) w.ask(nm.w_pre, 0, cols, nm.dtype);
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float a = p.h ? nm.h_scale * h[i][k] : 0.f;
+      v[i][k] = p.y ? fmaf(nm.y_scale, v[i][k], a) : a;
+    }
+  if (p.h_out) S::store(p.h_out, m * p.ldho, cols, p.h_dtype, v);
+  if (!p.x) return;
+  if (nm.pre) {
+    normalise<NV, VEC>(v, nm, red[2]);
+    weigh<NV, VEC>(v, nm, nm.w_pre, nm.b_pre, w);
+  }
+  S::store(p.x, m * p.ldx, cols, p.x_dtype, v);
+}
+
+// Rows too wide for the registers of a CTA: the row is read again for every
+// step.
+constexpr int kWideThreads = 1024;
+
 struct Stats {
   float mean, rstd;
 };
@@ -64,15 +278,15 @@ __device__ Stats row_stats(F value, const seedlm_norm& nm, float* red) {
   const float inv = 1.f / nm.cols;
   if (nm.kind == SEEDLM_NORM_LAYER) {
     float s = 0.f;
-    for (int j = threadIdx.x; j < nm.cols; j += blockDim.x) s += value(j);
+    for (int j = threadIdx.x; j < nm.cols; j += kWideThreads) s += value(j);
     st.mean = block_sum(s, red) * inv;
   }
   float s = 0.f;
-  for (int j = threadIdx.x; j < nm.cols; j += blockDim.x) {
+  for (int j = threadIdx.x; j < nm.cols; j += kWideThreads) {
     const float d = value(j) - st.mean;
     s = fmaf(d, d, s);
   }
-  st.rstd = rsqrtf(block_sum(s, red) * inv + nm.eps);
+  st.rstd = rsqrtf(block_sum(s, red + 32) * inv + nm.eps);
   return st;
 }
 
@@ -83,16 +297,15 @@ __device__ __forceinline__ float normed(float v, Stats st, const seedlm_norm& nm
   return v;
 }
 
-// One CTA a row; the row is read again for every step.
-__global__ void __launch_bounds__(256) block_norm_kernel(const NormArgs p) {
-  __shared__ float red[32];
+__global__ void __launch_bounds__(kWideThreads) block_norm_wide_kernel(const __grid_constant__ NormArgs p) {
+  __shared__ float red[4][32];
   grid_launch_dependents();
   grid_wait();
   const int64_t m = blockIdx.x;
   const seedlm_norm& nm = p.nm;
   Stats post{}, pre{};
   auto y = [&](int j) { return p.y[m * p.ldy + j]; };
-  if (p.y && nm.post) post = row_stats(y, nm, red);
+  if (p.y && nm.post) post = row_stats(y, nm, red[0]);
   auto hnew = [&](int j) {
     float r = p.h ? nm.h_scale * load_as(p.h, m * p.ldh + j, p.h_dtype) : 0.f;
     if (p.y) {
@@ -103,41 +316,123 @@ __global__ void __launch_bounds__(256) block_norm_kernel(const NormArgs p) {
     }
     return r;
   };
-  if (p.x && nm.pre) pre = row_stats(hnew, nm, red);
-  for (int j = threadIdx.x; j < nm.cols; j += blockDim.x) {
+  if (p.x && nm.pre) pre = row_stats(hnew, nm, red[2]);
+  for (int j = threadIdx.x; j < nm.cols; j += kWideThreads) {
     const float r = hnew(j);
     if (p.h_out) store_as(p.h_out, m * p.ldho + j, p.h_dtype, r);
     if (p.x) store_as(p.x, m * p.ldx + j, p.x_dtype, nm.pre ? normed(r, pre, nm, nm.w_pre, nm.b_pre, j) : r);
   }
 }
 
-__device__ __forceinline__ float activate(float g, int act) {
-  if (act == SEEDLM_SILU) return g / (1.f + expf(-g));
-  if (act == SEEDLM_GELU) return 0.5f * g * (1.f + erff(g * 0.70710678f));
-  return 0.5f * g * (1.f + tanhf(0.79788456f * (g + 0.044715f * g * g * g)));
+// ---------------------------------------------------------------------- glu
+
+// The sigmoid form of the tanh one: (1 + tanh z) / 2 = 1 / (1 + e^-2z).
+template <int ACT>
+__device__ __forceinline__ float activate(float g) {
+  if (ACT == SEEDLM_SILU) return g / (1.f + __expf(-g));
+  if (ACT == SEEDLM_GELU) return 0.5f * g * (1.f + erff(g * 0.70710678f));
+  return g / (1.f + __expf(-1.5957691f * (g + 0.044715f * g * g * g)));
 }
 
-__global__ void __launch_bounds__(256) glu_kernel(int cols, int act, const float* __restrict__ GU, int64_t ldgu, void* X,
-                                                  int64_t ldx, int x_dtype) {
+constexpr int kGluThreads = 256, kGluGroups = 2;  // groups of four outputs a thread
+
+template <int ACT, bool VEC>
+__global__ void __launch_bounds__(kGluThreads)
+glu_kernel(int cols, int chunks, const float* __restrict__ GU, int64_t ldgu, void* __restrict__ X, int64_t ldx, int x_dtype) {
   grid_launch_dependents();
+  const int64_t m = blockIdx.x / chunks;
+  const int first = (int)(blockIdx.x % chunks) * (4 * kGluThreads * kGluGroups);
+  const float* G = GU + m * ldgu;
   grid_wait();
-  const int64_t m = blockIdx.x;
-  for (int j = threadIdx.x; j < cols; j += blockDim.x)
-    store_as(X, m * ldx + j, x_dtype, activate(GU[m * ldgu + j], act) * GU[m * ldgu + cols + j]);
+  __align__(16) float g[kGluGroups][4], u[kGluGroups][4];
+#pragma unroll
+  for (int i = 0; i < kGluGroups; ++i) {
+    const int j = first + (VEC ? 4 : 1) * (int)threadIdx.x + 4 * kGluThreads * i;
+    if (VEC) {
+      if (j < cols) {
+        *reinterpret_cast<float4*>(g[i]) = *reinterpret_cast<const float4*>(G + j);
+        *reinterpret_cast<float4*>(u[i]) = *reinterpret_cast<const float4*>(G + cols + j);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j + kGluThreads * k < cols) {
+          g[i][k] = G[j + kGluThreads * k];
+          u[i][k] = G[cols + j + kGluThreads * k];
+        }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kGluGroups; ++i) {
+    const int j = first + (VEC ? 4 : 1) * (int)threadIdx.x + 4 * kGluThreads * i;
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = activate<ACT>(g[i][k]) * u[i][k];
+    if (VEC) {
+      const bool bf16 = x_dtype == SEEDLM_BF16;
+      if (j < cols)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(X) + m * ldx + j) =
+            make_uint2(two_to(v[0], v[1], bf16), two_to(v[2], v[3], bf16));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j + kGluThreads * k < cols) store_as(X, m * ldx + j + kGluThreads * k, x_dtype, v[k]);
+    }
+  }
+}
+
+// Whether rows can be read or written four elements at a time.
+bool rows_of_four(const void* p, int64_t ld, int dtype) {
+  return !p || (aligned(p, dtype == SEEDLM_F32 ? 16 : 8) && ld % 4 == 0);
+}
+
+template <int NV>
+int launch_rows(const NormArgs& p, int M, int threads, bool vec, cudaStream_t stream) {
+  return vec ? launch_pdl(block_norm_kernel<NV, true>, M, threads, 0, stream, p)
+             : launch_pdl(block_norm_kernel<NV, false>, M, threads, 0, stream, p);
+}
+
+template <int ACT>
+int launch_glu_act(int M, int cols, const float* GU, int64_t ldgu, void* X, int64_t ldx, int x_dtype,
+                   cudaStream_t stream) {
+  const bool vec = cols % 4 == 0 && rows_of_four(GU, ldgu, SEEDLM_F32) && rows_of_four(X, ldx, x_dtype);
+  const int chunks = (cols + 4 * kGluThreads * kGluGroups - 1) / (4 * kGluThreads * kGluGroups);
+  if ((int64_t)M * chunks > INT32_MAX) return SEEDLM_EUNSUPPORTED;
+  auto kernel = vec ? glu_kernel<ACT, true> : glu_kernel<ACT, false>;
+  return launch_pdl(kernel, (unsigned)(M * chunks), kGluThreads, 0, stream, cols, chunks, GU, ldgu, X, ldx, x_dtype);
 }
 
 }  // namespace
 
 int launch_block_norm(const seedlm_norm& nm, int M, const float* y, int64_t ldy, const void* gate, int64_t ldg,
                       const void* h, int64_t ldh, void* h_out, int64_t ldho, int h_dtype, void* x, int64_t ldx,
-                      int x_dtype, cudaStream_t stream, const DeviceInfo&) {
+                      int x_dtype, cudaStream_t stream, const DeviceInfo& dev) {
   NormArgs p{nm, y, ldy, gate, ldg, h, ldh, h_out, ldho, h_dtype, x, ldx, x_dtype};
-  return launch_pdl(block_norm_kernel, M, 256, 0, stream, p);
+  const int cols = nm.cols, groups = (cols + 3) / 4;
+  if (groups > 8 * kRowThreads<8>) return launch_pdl(block_norm_wide_kernel, M, kWideThreads, 0, stream, p);
+  const bool vec = cols % 4 == 0 && rows_of_four(y, ldy, SEEDLM_F32) && rows_of_four(gate, ldg, nm.dtype) &&
+                   rows_of_four(h, ldh, h_dtype) && rows_of_four(h_out, ldho, h_dtype) &&
+                   rows_of_four(x, ldx, x_dtype) && rows_of_four(nm.w_post, 0, nm.dtype) &&
+                   rows_of_four(nm.b_post, 0, nm.dtype) && rows_of_four(nm.w_pre, 0, nm.dtype) &&
+                   rows_of_four(nm.b_pre, 0, nm.dtype);
+  // Few rows: as many threads as there are, for the latency of one row.  Many:
+  // CTAs of 256 threads, of which several fit an SM and take turns between
+  // memory and sums.
+  const int most = M <= 2 * dev.num_sms ? 1024 : 256;
+  int nv = 1;
+  while (nv < (most == 256 ? 8 : 4) && groups > nv * most) nv *= 2;
+  const int threads = ((groups + nv - 1) / nv + 31) / 32 * 32;
+  return nv == 1   ? launch_rows<1>(p, M, threads, vec, stream)
+         : nv == 2 ? launch_rows<2>(p, M, threads, vec, stream)
+         : nv == 4 ? launch_rows<4>(p, M, threads, vec, stream)
+                   : launch_rows<8>(p, M, threads, vec, stream);
 }
 
 int launch_glu(int M, int cols, int act, const float* GU, int64_t ldgu, void* X, int64_t ldx, int x_dtype,
                cudaStream_t stream, const DeviceInfo&) {
-  return launch_pdl(glu_kernel, M, 256, 0, stream, cols, act, GU, ldgu, X, ldx, x_dtype);
+  return act == SEEDLM_SILU   ? launch_glu_act<SEEDLM_SILU>(M, cols, GU, ldgu, X, ldx, x_dtype, stream)
+         : act == SEEDLM_GELU ? launch_glu_act<SEEDLM_GELU>(M, cols, GU, ldgu, X, ldx, x_dtype, stream)
+                              : launch_glu_act<SEEDLM_GELU_TANH>(M, cols, GU, ldgu, X, ldx, x_dtype, stream);
 }
 
 }  // namespace seedlm
