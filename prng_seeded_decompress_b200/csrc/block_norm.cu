@@ -5,6 +5,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "launch.cuh"
 #include "seedlm_device.cuh"
 #include "seedlm_internal.h"
@@ -71,28 +73,36 @@ struct NormArgs {
   int x_dtype;
 };
 
+// The 16-bit type of a call: 0 fp16, 1 bf16, 2 only known element by element.
+template <int T16>
+__device__ __forceinline__ bool is_bf16(int dtype) {
+  return T16 == 2 ? dtype == SEEDLM_BF16 : T16 == 1;
+}
+
 // A thread's share of a row: NV groups of four elements, neighbouring ones
 // (VEC) or, where rows are not aligned for that, ones a CTA's width apart.  The
 // type is looked at once for a share, so that all its loads are in flight
 // together.
-template <int NV, bool VEC>
+template <int NV, bool VEC, int T16 = 2, bool FULL = false>
 struct Share {
   __device__ static int index(int i, int k) {
     return VEC ? 4 * ((int)threadIdx.x + (int)blockDim.x * i) + k : (int)threadIdx.x + (int)blockDim.x * (4 * i + k);
   }
+  // Whether the element lies in the row; FULL: the CTA's threads end with it.
+  __device__ static bool in(int i, int k, int cols) { return FULL || index(i, k) < cols; }
   // 16-bit elements as they are stored; zeros beyond the row.
   __device__ static void load16(const void* p, int64_t row, int cols, uint2 (&raw)[NV]) {
     const uint16_t* from = static_cast<const uint16_t*>(p) + row;
     if (VEC) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        raw[i] = index(i, 0) < cols ? *reinterpret_cast<const uint2*>(from + index(i, 0)) : make_uint2(0u, 0u);
+        raw[i] = in(i, 0, cols) ? *reinterpret_cast<const uint2*>(from + index(i, 0)) : make_uint2(0u, 0u);
     } else {
       uint16_t e[NV][4];
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) e[i][k] = index(i, k) < cols ? from[index(i, k)] : (uint16_t)0;
+        for (int k = 0; k < 4; ++k) e[i][k] = in(i, k, cols) ? from[index(i, k)] : (uint16_t)0;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         raw[i] = make_uint2(e[i][0] | (uint32_t)e[i][1] << 16, e[i][2] | (uint32_t)e[i][3] << 16);
@@ -103,11 +113,11 @@ struct Share {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (VEC) {
-        const float4 a = index(i, 0) < cols ? *reinterpret_cast<const float4*>(from + index(i, 0)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 a = in(i, 0, cols) ? *reinterpret_cast<const float4*>(from + index(i, 0)) : make_float4(0.f, 0.f, 0.f, 0.f);
         v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
       } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[i][k] = index(i, k) < cols ? from[index(i, k)] : 0.f;
+        for (int k = 0; k < 4; ++k) v[i][k] = in(i, k, cols) ? from[index(i, k)] : 0.f;
       }
     }
   }
@@ -124,26 +134,26 @@ struct Share {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (VEC) {
-          if (index(i, 0) < cols)
+          if (in(i, 0, cols))
             *reinterpret_cast<float4*>(to + index(i, 0)) = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (index(i, k) < cols) to[index(i, k)] = v[i][k];
+            if (in(i, k, cols)) to[index(i, k)] = v[i][k];
         }
     } else {
       uint16_t* to = static_cast<uint16_t*>(p) + row;
-      const bool bf16 = dtype == SEEDLM_BF16;
+      const bool bf16 = is_bf16<T16>(dtype);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const uint2 a = make_uint2(two_to(v[i][0], v[i][1], bf16), two_to(v[i][2], v[i][3], bf16));
         if (VEC) {
-          if (index(i, 0) < cols) *reinterpret_cast<uint2*>(to + index(i, 0)) = a;
+          if (in(i, 0, cols)) *reinterpret_cast<uint2*>(to + index(i, 0)) = a;
         } else {
           const uint32_t w[2] = {a.x, a.y};
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (index(i, k) < cols) to[index(i, k)] = (uint16_t)(w[k / 2] >> (16 * (k % 2)));
+            if (in(i, k, cols)) to[index(i, k)] = (uint16_t)(w[k / 2] >> (16 * (k % 2)));
         }
       }
     }
@@ -152,20 +162,21 @@ struct Share {
 
 // A share of some type, asked for early and used late: 16-bit elements wait in
 // registers as they are; fp32 ones would take too many and are loaded when used.
-template <int NV, bool VEC>
+template <int NV, bool VEC, int T16 = 2, bool FULL = false>
 struct Early {
+  using S = Share<NV, VEC, T16, FULL>;
   uint2 raw[NV];
   __device__ void ask(const void* p, int64_t row, int cols, int dtype) {
-    if (p && dtype != SEEDLM_F32) Share<NV, VEC>::load16(p, row, cols, raw);
+    if (p && dtype != SEEDLM_F32) S::load16(p, row, cols, raw);
   }
   __device__ void use(const void* p, int64_t row, int cols, int dtype, float (&v)[NV][4]) const {
-    if (dtype != SEEDLM_F32) Share<NV, VEC>::widen(raw, dtype == SEEDLM_BF16, v);
-    else Share<NV, VEC>::load32(p, row, cols, v);
+    if (dtype != SEEDLM_F32) S::widen(raw, is_bf16<T16>(dtype), v);
+    else S::load32(p, row, cols, v);
   }
 };
 
 // v <- norm(v), all but weights and bias; two passes over registers.
-template <int NV, bool VEC>
+template <class S, int NV>
 __device__ __forceinline__ void normalise(float (&v)[NV][4], const seedlm_norm& nm, float* red) {
   const float inv = 1.f / nm.cols;
   if (nm.kind == SEEDLM_NORM_LAYER) {
@@ -176,7 +187,7 @@ __device__ __forceinline__ void normalise(float (&v)[NV][4], const seedlm_norm& 
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[i][k] = Share<NV, VEC>::index(i, k) < nm.cols ? v[i][k] - mean : 0.f;
+      for (int k = 0; k < 4; ++k) v[i][k] = S::in(i, k, nm.cols) ? v[i][k] - mean : 0.f;
   }
   float s = 0.f;
 #pragma unroll
@@ -189,9 +200,9 @@ __device__ __forceinline__ void normalise(float (&v)[NV][4], const seedlm_norm& 
     for (int k = 0; k < 4; ++k) v[i][k] *= rstd;
 }
 
-template <int NV, bool VEC>
+template <class E, int NV>
 __device__ __forceinline__ void weigh(float (&v)[NV][4], const seedlm_norm& nm, const void* w, const void* b,
-                                      const Early<NV, VEC>& early_w) {
+                                      const E& early_w) {
   float t[NV][4];
   if (w) {
     early_w.use(w, 0, nm.cols, nm.dtype, t);
@@ -201,7 +212,7 @@ __device__ __forceinline__ void weigh(float (&v)[NV][4], const seedlm_norm& nm, 
       for (int k = 0; k < 4; ++k) v[i][k] *= nm.weight_offset + t[i][k];
   }
   if (b) {
-    Early<NV, VEC> late;
+    E late;
     late.ask(b, 0, nm.cols, nm.dtype);
     late.use(b, 0, nm.cols, nm.dtype, t);
 #pragma unroll
@@ -213,11 +224,10 @@ __device__ __forceinline__ void weigh(float (&v)[NV][4], const seedlm_norm& nm, 
 
 // One CTA a row, which stays in registers: y and h are read once, h' and x
 // written once.
-template <int NV>
-constexpr int kRowThreads = NV == 8 ? 512 : 1024;
+constexpr int kRowThreads = 1024;
 
 template <int NV, bool VEC>
-__global__ void __launch_bounds__(kRowThreads<NV>) block_norm_kernel(const __grid_constant__ NormArgs p) {
+__global__ void __launch_bounds__(kRowThreads) block_norm_kernel(const __grid_constant__ NormArgs p) {
   __shared__ float red[4][32];  // one place for each sum of a row
   const seedlm_norm& nm = p.nm;
   const int cols = nm.cols;
@@ -235,8 +245,8 @@ __global__ void __launch_bounds__(kRowThreads<NV>) block_norm_kernel(const __gri
   stream.ask(p.h, m * p.ldh, cols, p.h_dtype);
   if (p.y) {
     if (nm.post) {
-      normalise<NV, VEC>(v, nm, red[0]);
-      weigh<NV, VEC>(v, nm, nm.w_post, nm.b_post, w);
+      normalise<S>(v, nm, red[0]);
+      weigh(v, nm, nm.w_post, nm.b_post, w);
     }
     if (p.gate) {
       gate.use(p.gate, m * p.ldg, cols, nm.dtype, h);
@@ -258,10 +268,137 @@ __global__ void __launch_bounds__(kRowThreads<NV>) block_norm_kernel(const __gri
   if (p.h_out) S::store(p.h_out, m * p.ldho, cols, p.h_dtype, v);
   if (!p.x) return;
   if (nm.pre) {
-    normalise<NV, VEC>(v, nm, red[2]);
-    weigh<NV, VEC>(v, nm, nm.w_pre, nm.b_pre, w);
+    normalise<S>(v, nm, red[2]);
+    weigh(v, nm, nm.w_pre, nm.b_pre, w);
   }
   S::store(p.x, m * p.ldx, cols, p.x_dtype, v);
+}
+
+// Many rows: each CTA goes through rows a grid apart, with the next row coming
+// into shared memory while it sums up this one, so that memory is not left idle.
+// A thread copies exactly what it will itself read, as soon as it has taken the
+// row before out of the same place, so the copies need no barrier.  256 threads
+// hold a row of 8192; the CTAs of an SM wait for their sums in turn.
+constexpr int kStreamGroups = 8, kStreamThreads = 256, kStreamSums = 2 * 4 * 32 * 4;
+
+// Asynchronous copy of 8 or 16 bytes to shared memory.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(from) : "memory");
+}
+
+template <bool H32, int T16, bool FULL>
+__global__ void __launch_bounds__(kStreamThreads, 2)
+block_norm_stream_kernel(const __grid_constant__ NormArgs p, int M) {
+  constexpr int NV = kStreamGroups, HB = H32 ? 16 : 8;
+  extern __shared__ __align__(16) unsigned char shared[];
+  float(*red)[4][32] = reinterpret_cast<float(*)[4][32]>(shared);  // [2]: sums of this row and the next
+  const seedlm_norm& nm = p.nm;
+  const int cols = nm.cols, threads = blockDim.x;
+  using S = Share<NV, true, T16, FULL>;
+  using E = Early<NV, true, T16, FULL>;
+  const bool pre = p.x && nm.pre, post = p.y && nm.post, gates = p.y && p.gate;
+  const bool gate_row = gates && p.ldg != 0 && nm.dtype != SEEDLM_F32;  // others are read when used
+  // Places of this thread's groups of y, h and gate.
+  unsigned char* y_at = shared + kStreamSums + threadIdx.x * 16;
+  unsigned char* h_at = shared + kStreamSums + NV * threads * 16 + threadIdx.x * HB;
+  unsigned char* g_at = shared + kStreamSums + NV * threads * (16 + HB) + threadIdx.x * 8;
+  auto fetch_y = [&](int64_t m) {
+    if (p.y && m < M) {
+      const float* from = p.y + m * p.ldy;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (S::in(i, 0, cols)) copy_async<16>(y_at + i * threads * 16, from + S::index(i, 0));
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto fetch_rest = [&](int64_t m) {
+    if (p.h && m < M) {
+      const unsigned char* from = static_cast<const unsigned char*>(p.h) + m * p.ldh * (HB / 4);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (S::in(i, 0, cols)) copy_async<HB>(h_at + i * threads * HB, from + S::index(i, 0) * (HB / 4));
+    }
+    if (gate_row && m < M) {
+      const uint16_t* from = static_cast<const uint16_t*>(p.gate) + m * p.ldg;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (S::in(i, 0, cols)) copy_async<8>(g_at + i * threads * 8, from + S::index(i, 0));
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // Takes the 16-bit groups at `at` (zeros beyond the row).
+  auto take16 = [&](const unsigned char* at, bool bf16, float (&v)[NV][4]) {
+    uint2 raw[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      raw[i] = S::in(i, 0, cols) ? *reinterpret_cast<const uint2*>(at + i * threads * 8) : make_uint2(0u, 0u);
+    S::widen(raw, bf16, v);
+  };
+  auto take32 = [&](const unsigned char* at, float (&v)[NV][4]) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float4 a = S::in(i, 0, cols) ? *reinterpret_cast<const float4*>(at + i * threads * 16) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
+    }
+  };
+  grid_launch_dependents();
+  grid_wait();
+  fetch_y(blockIdx.x);
+  fetch_rest(blockIdx.x);
+  int parity = 0;
+  for (int64_t m = blockIdx.x; m < M; m += gridDim.x, parity ^= 1) {
+    float v[NV][4], t[NV][4];
+    E w;
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    if (p.y) {
+      take32(y_at, v);
+      fetch_y(m + gridDim.x);
+      if (post) {
+        w.ask(nm.w_post, 0, cols, nm.dtype);
+        normalise<S>(v, nm, red[parity][0]);
+        weigh(v, nm, nm.w_post, nm.b_post, w);
+      }
+    } else {
+      fetch_y(M);
+    }
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    if (gates) {
+      if (gate_row) {
+        take16(g_at, is_bf16<T16>(nm.dtype), t);
+      } else {
+        E late;
+        late.ask(p.gate, m * p.ldg, cols, nm.dtype);
+        late.use(p.gate, m * p.ldg, cols, nm.dtype, t);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[i][k] *= t[i][k];
+    }
+    if (p.h) {
+      if (H32) take32(h_at, t);
+      else take16(h_at, is_bf16<T16>(p.h_dtype), t);
+    }
+    fetch_rest(m + gridDim.x);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float a = p.h ? nm.h_scale * t[i][k] : 0.f;
+        v[i][k] = p.y ? fmaf(nm.y_scale, v[i][k], a) : a;
+      }
+    if (p.h_out) S::store(p.h_out, m * p.ldho, cols, H32 ? SEEDLM_F32 : p.h_dtype, v);
+    if (!p.x) continue;
+    if (pre) {
+      w.ask(nm.w_pre, 0, cols, nm.dtype);
+      normalise<S>(v, nm, red[parity][2]);
+      weigh(v, nm, nm.w_pre, nm.b_pre, w);
+    }
+    S::store(p.x, m * p.ldx, cols, p.x_dtype, v);
+  }
 }
 
 // Rows too wide for the registers of a CTA: the row is read again for every
@@ -392,6 +529,20 @@ int launch_rows(const NormArgs& p, int M, int threads, bool vec, cudaStream_t st
              : launch_pdl(block_norm_kernel<NV, false>, M, threads, 0, stream, p);
 }
 
+template <bool H32, int T16>
+int launch_stream(const NormArgs& p, int M, cudaStream_t stream, const DeviceInfo& dev) {
+  const int cols = p.nm.cols;
+  const int threads = ((cols / 4 + kStreamGroups - 1) / kStreamGroups + 31) / 32 * 32;
+  const int smem = kStreamSums + kStreamGroups * threads * (16 + (H32 ? 16 : 8) + (p.y && p.gate && p.ldg != 0 ? 8 : 0));
+  auto kernel = cols == 4 * kStreamGroups * threads ? block_norm_stream_kernel<H32, T16, true>
+                                                    : block_norm_stream_kernel<H32, T16, false>;
+  const int rc = allow_max_smem((const void*)kernel, dev);
+  if (rc) return rc;
+  // As many CTAs as an SM holds at 128 registers a thread.
+  const int ctas = std::max(1, std::min(2 * kStreamThreads / threads, 227 * 1024 / (smem + 1024)));
+  return launch_pdl(kernel, std::min<int64_t>(M, (int64_t)ctas * dev.num_sms), threads, (size_t)smem, stream, p, M);
+}
+
 template <int ACT>
 int launch_glu_act(int M, int cols, const float* GU, int64_t ldgu, void* X, int64_t ldx, int x_dtype,
                    cudaStream_t stream) {
@@ -409,23 +560,32 @@ int launch_block_norm(const seedlm_norm& nm, int M, const float* y, int64_t ldy,
                       int x_dtype, cudaStream_t stream, const DeviceInfo& dev) {
   NormArgs p{nm, y, ldy, gate, ldg, h, ldh, h_out, ldho, h_dtype, x, ldx, x_dtype};
   const int cols = nm.cols, groups = (cols + 3) / 4;
-  if (groups > 8 * kRowThreads<8>) return launch_pdl(block_norm_wide_kernel, M, kWideThreads, 0, stream, p);
+  if (groups > 4 * kRowThreads) return launch_pdl(block_norm_wide_kernel, M, kWideThreads, 0, stream, p);
   const bool vec = cols % 4 == 0 && rows_of_four(y, ldy, SEEDLM_F32) && rows_of_four(gate, ldg, nm.dtype) &&
                    rows_of_four(h, ldh, h_dtype) && rows_of_four(h_out, ldho, h_dtype) &&
                    rows_of_four(x, ldx, x_dtype) && rows_of_four(nm.w_post, 0, nm.dtype) &&
                    rows_of_four(nm.b_post, 0, nm.dtype) && rows_of_four(nm.w_pre, 0, nm.dtype) &&
                    rows_of_four(nm.b_pre, 0, nm.dtype);
   // Few rows: as many threads as there are, for the latency of one row.  Many:
-  // CTAs of 256 threads, of which several fit an SM and take turns between
-  // memory and sums.
-  const int most = M <= 2 * dev.num_sms ? 1024 : 256;
+  // fewer threads with more of a row each, and the next row on its way.
+  if (vec && M > 2 * dev.num_sms && groups <= kStreamGroups * kStreamThreads) {
+    const bool h32 = (h || h_out) && h_dtype == SEEDLM_F32;
+    // The one 16-bit type of the call, if it has one.
+    int t16 = x ? x_dtype : SEEDLM_F32;
+    for (int t : {h || h_out ? h_dtype : SEEDLM_F32, nm.dtype})
+      if (t != SEEDLM_F32) t16 = t16 == SEEDLM_F32 || t16 == t ? t : 3;
+    if (t16 == SEEDLM_F16)
+      return h32 ? launch_stream<true, 0>(p, M, stream, dev) : launch_stream<false, 0>(p, M, stream, dev);
+    if (t16 == SEEDLM_BF16)
+      return h32 ? launch_stream<true, 1>(p, M, stream, dev) : launch_stream<false, 1>(p, M, stream, dev);
+    return h32 ? launch_stream<true, 2>(p, M, stream, dev) : launch_stream<false, 2>(p, M, stream, dev);
+  }
   int nv = 1;
-  while (nv < (most == 256 ? 8 : 4) && groups > nv * most) nv *= 2;
+  while (groups > nv * kRowThreads) nv *= 2;
   const int threads = ((groups + nv - 1) / nv + 31) / 32 * 32;
   return nv == 1   ? launch_rows<1>(p, M, threads, vec, stream)
          : nv == 2 ? launch_rows<2>(p, M, threads, vec, stream)
-         : nv == 4 ? launch_rows<4>(p, M, threads, vec, stream)
-                   : launch_rows<8>(p, M, threads, vec, stream);
+                   : launch_rows<4>(p, M, threads, vec, stream);
 }
 
 int launch_glu(int M, int cols, int act, const float* GU, int64_t ldgu, void* X, int64_t ldx, int x_dtype,
