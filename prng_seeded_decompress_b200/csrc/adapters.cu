@@ -232,8 +232,7 @@ adapters_plan_kernel(int M, int n, int T, const int32_t* __restrict__ ids, int32
 // adapter wastes tensor work, of which there is plenty, and no memory traffic,
 // which is what bounds both kernels.
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;  // of the kernels for tall tiles
-constexpr int kLowWarps = 4;                       // of those for low ones
+constexpr int kLowWarps = 4;   // of the kernels for low tiles
 constexpr int kStep = 32;      // contraction elements of one 16-byte load per lane
 constexpr int kTall = 64;      // rows of a tall tile
 constexpr int kMaxSplits = 8;  // CTAs of a cluster that share the first contraction
@@ -273,11 +272,21 @@ struct ApplyArgs {
 
 __device__ __forceinline__ const int32_t* plan_tail_of(const ApplyArgs& p) { return p.plan + plan_tail(p.M, p.ad.n); }
 
-__device__ __forceinline__ bool plan_fits(const ApplyArgs& p) {
-  const int32_t* tail = plan_tail_of(p);
-  const bool ok = tail[0] == p.M && tail[1] == p.ad.n;
-  if (!ok && threadIdx.x == 0) atomicOr(&g_plan_mismatch, 1u);
-  return ok;
+// The plan's head, {M, n, tiles with an adapter, tiles}, with no tiles at all if
+// it does not belong to this call.
+__device__ __forceinline__ int4 plan_head(const ApplyArgs& p) {
+  int4 head = *reinterpret_cast<const int4*>(plan_tail_of(p));
+  if (head.x != p.M || head.y != p.ad.n) {
+    if (threadIdx.x == 0) atomicOr(&g_plan_mismatch, 1u);
+    head.z = head.w = 0;
+  }
+  return head;
+}
+
+// Tile t {adapter or -1, first, rows, 0}; t below the plan's room, whether the
+// plan has so many or not.
+__device__ __forceinline__ int4 plan_tile(const ApplyArgs& p, int64_t t) {
+  return reinterpret_cast<const int4*>(plan_tail_of(p))[1 + t];
 }
 
 __device__ __forceinline__ int rank_of(const seedlm_adapters& ad, int a) {
@@ -384,12 +393,13 @@ __device__ __forceinline__ void store_sums(const ApplyArgs& p, const float* sums
       const int j = j0 + 2 * lane;
       const int slot = slot0 + j, s = slot / p.slots, r = slot - s * p.slots;
       const bool in = j < N && s < p.ad.slices;
-      float2 v = make_float2(0.f, 0.f);
-      if (in)
-        for (int c = 0; c < ctas; ++c) {
-          const float2 add = load_of_cta(sums + i * stride + j, c);
-          v = make_float2(v.x + add.x, v.y + add.y);
-        }
+      float2 v = make_float2(0.f, 0.f), part[kMaxSplits];
+#pragma unroll
+      for (int c = 0; c < kMaxSplits; ++c)  // all on their way together
+        if (in && c < ctas) part[c] = load_of_cta(sums + i * stride + j, c);
+#pragma unroll
+      for (int c = 0; c < kMaxSplits; ++c)
+        if (in && c < ctas) v = make_float2(v.x + part[c].x, v.y + part[c].y);
       // Beyond the adapter's rank rows of zeros met x, which gives NaN where x
       // has infinities.
       v = make_float2(r < rank ? v.x * scale : 0.f, r + 1 < rank ? v.y * scale : 0.f);
@@ -437,23 +447,22 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
   // After the wait: what ran before this kernel is then complete for the next
   // one too, which reads the plan, B and base before its own wait.
   grid_launch_dependents();
-  if (!plan_fits(p)) return;
-  const int32_t* tail = plan_tail_of(p);
   const int cluster = blockIdx.x / (int)cluster_size();
   const int group = cluster % p.groups, s = cluster / p.groups % p.ad.slices, t = cluster / (p.groups * p.ad.slices);
-  if (t >= tail[2]) return;
-  const int4 tile = reinterpret_cast<const int4*>(tail)[1 + t];
+  const int4 tile = plan_tile(p, t), head = plan_head(p);
+  if (t >= head.z) return;
   const int a = tile.x, first = tile.y, count = tile.z;
-  const int r0 = group * R, rank = rank_of(p.ad, a) - r0;  // of this group
-  if (rank <= 0) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
+  const int row = g < count ? p.plan[first + g] : -1;
+  const int r0 = group * R, rank = rank_of(p.ad, a) - r0;  // of this group
+  const float scale = p.ad.scales ? p.ad.scales[a] : 1.f;
+  if (rank <= 0) return;
   const int k0 = (int)cluster_rank() * p.split_cols, k1 = min(p.ad.cols, k0 + p.split_cols);
   const bool vec = (p.vec_a >> s) & (p.vec_a >> SEEDLM_MAX_SLICES) & 1;
   const int blocks = min(RB, (rank + 15) / 16);
 
   // Row g of the tile and rows 8 j + g of A, at this lane's place in the part.
   const int64_t a_row = p.ad.a_row[s];
-  const int row = g < count ? p.plan[first + g] : -1;
   const bool have_x = row >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, row, p.M);
   const int k_first = k0 + warp * kStep + 8 * q;
   const uint16_t* x = p.X + (have_x ? row * p.ldx : 0) + k_first;
@@ -532,142 +541,160 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
     for (int w = 0; w < kLowWarps; ++w) sum += red[(w * R + r) * 9 + i];
     sums[i * R + r] = sum;
   }
-  store_sums<BF16, R>(p, sums, R, first, count, r0 + rank, s * p.slots + r0, p.ad.scales ? p.ad.scales[a] : 1.f);
+  store_sums<BF16, R>(p, sums, R, first, count, r0 + rank, s * p.slots + r0, scale);
 }
 
-// S for tall tiles (64 rows): a cluster takes one tile and NG slots of the
-// slices laid end to end, each of its CTAs one part of the columns.  Rows of X
-// and A come through a ring of shared-memory stages of 64 columns, and the
-// warps share the products out WR x WT, so that X is read once for NG slots and
-// no sums cross warps.  A row of a stage is 128 bytes, 8 units of 16; odd rows
-// have their halves swapped, so that 8 neighbouring lanes (2 rows x 4 units)
-// touch every bank once.
-constexpr int kStages = 4, kStageCols = 64;
+// S for tall tiles (64 rows) on tcgen05.mma: a cluster takes one tile and 128
+// slots of the slices laid end to end (rows of A, the 128-row operand), each of
+// its CTAs one part of the columns, 64 at a time through a ring of shared-memory
+// stages.  Bound by the traffic from L2 (A again for every tile).  The tensor
+// cores cut off what an addition leaves below a sum's last bit, so the stages go
+// to four sums in turn, which are added in fp32, rounded.
+struct ShrinkTallLayout {
+  static constexpr int kThreads = 128, kStages = 4, kCols = 64, kSlots = 128, kSums = 4;
+  static constexpr int kStageBytes = (kSlots + kTall) * 128;   // rows of A, then rows of X
+  static constexpr int kBars = kStages * kStageBytes;          // a stage's products are done
+  static constexpr int kBytes = kBars + kStages * 8 + 8;       // tensor memory's address, give-up flag
+  static constexpr int kColumns = kSums * kTall;
+  static constexpr int kSumStride = kSlots + 4;
+};
+// A product of one tile takes microseconds; a wait this long never ends.
+constexpr uint64_t kTallWaitLimit = 2000000000ull;
 
-template <bool BF16, int NG, int WR>
-__global__ void __launch_bounds__(kThreads, 2) adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
-  constexpr int WT = kWarps / WR, RB = NG / 16 / WR, NT = kTall / 8 / WT;
-  static_assert(RB >= 1 && NT >= 1 && WR * RB * 16 == NG && WT * NT * 8 == kTall, "shares");
-  extern __shared__ __align__(128) unsigned char smem[];
-  constexpr int kStageRows = kTall + NG, kStageBytes = kStageRows * 128;
-  constexpr int kSumStride = NG + 4;
-  static_assert(kTall * kSumStride * 4 <= kStages * kStageBytes, "the sums lie over the stages");
+template <bool BF16>
+__global__ void __launch_bounds__(ShrinkTallLayout::kThreads, 2)
+adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
+  using L = ShrinkTallLayout;
+  static_assert(kTall * L::kSumStride * 4 <= L::kBars, "the sums lie over the stages");
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const uint32_t bars = tc::smem_u32(smem + L::kBars);
+  volatile uint32_t* slot = reinterpret_cast<uint32_t*>(smem + L::kBars + L::kStages * 8);
+  // Tensor memory before the next kernel may start: one that takes all of it and
+  // then waits for this one must not come first.
+  if (warp == 0) tc::tmem_alloc(tc::smem_u32(smem + L::kBars + L::kStages * 8), L::kColumns);
+  if (tid == 32) {
+    for (int i = 0; i < L::kStages; ++i) tc::mbar_init(bars + 8 * i, 1);
+    tc::fence_mbar_init();
+    slot[1] = 0;
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = slot[0];
   grid_wait();
   grid_launch_dependents();  // after the wait, as above
-  if (!plan_fits(p)) return;
-  const int32_t* tail = plan_tail_of(p);
   const int cluster = blockIdx.x / (int)cluster_size();
   const int group = cluster % p.groups, t = cluster / p.groups;
-  if (t >= tail[2]) return;
-  const int4 tile = reinterpret_cast<const int4*>(tail)[1 + t];
-  const int a = tile.x, first = tile.y, count = tile.z;
-  const int rank = rank_of(p.ad, a), cols = p.ad.cols;
-  const int k0 = (int)cluster_rank() * p.split_cols, k1 = min(cols, k0 + p.split_cols);
-  const int steps = k1 > k0 ? (k1 - k0 + kStageCols - 1) / kStageCols : 0;
+  const int4 tile = plan_tile(p, t), head = plan_head(p);
+  bool ok = true;
+  if (t < head.z) {  // the same in all CTAs of a cluster
+    const int a = tile.x, first = tile.y, count = tile.z;
+    const int rank = rank_of(p.ad, a);
+    const int k0 = (int)cluster_rank() * p.split_cols, k1 = min(p.ad.cols, k0 + p.split_cols);
+    const int steps = k1 > k0 ? (k1 - k0 + L::kCols - 1) / L::kCols : 0;
 
-  // This thread's rows of every stage: unit `unit` of rows row0, row0 + 32, ...
-  constexpr int kMine = kStageRows * 8 / kThreads;
-  static_assert(kStageRows * 8 % kThreads == 0, "units");
-  const int unit = threadIdx.x % 8, row0 = threadIdx.x / 8;
-  const uint16_t* src[kMine];  // at this thread's place in the stage to be fetched next
-  int bytes[kMine];            // 16, or 0 where there is no such row
-  unsigned vec = 0;
+    // This thread's rows of every stage: unit `unit` of rows row0, row0 + 16, ...
+    // of A (the first eight) and X (the others).  Rows that are not there are
+    // zeroed once in all stages and not copied.
+    constexpr int kMine = (L::kSlots + kTall) / 16;
+    const int unit = tid % 8, row0 = tid / 8;
+    const int place = row0 * 128 + (unit ^ (row0 & 7)) * 16;
+    const uint16_t* src[kMine];
+    unsigned there = 0, vec = 0;
 #pragma unroll
-  for (int i = 0; i < kMine; ++i) {
-    const int row = row0 + 32 * i;
-    src[i] = p.X;
-    bytes[i] = 0;
-    bool aligned16 = true;
-    if (row < kTall) {
-      const int m = row < count ? p.plan[first + row] : -1;
-      if (m >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, m, p.M)) {
-        src[i] = p.X + m * p.ldx;
-        bytes[i] = 16;
-        aligned16 = p.vec_a >> SEEDLM_MAX_SLICES & 1;
+    for (int i = 0; i < kMine; ++i) {
+      const int row = row0 + 16 * i;
+      src[i] = nullptr;
+      if (row < L::kSlots) {
+        const int place_of = group * L::kSlots + row, s = place_of / p.slots, r = place_of - s * p.slots;
+        if (s < p.ad.slices && r < rank) {
+          src[i] = static_cast<const uint16_t*>(p.ad.A[s]) + a * p.ad.a_adapter[s] + r * p.ad.a_row[s] + k0 + 8 * unit;
+          vec |= (unsigned)(p.vec_a >> s & 1) << i;
+        }
+      } else {
+        const int m = row - L::kSlots < count ? p.plan[first + row - L::kSlots] : -1;
+        if (m >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, m, p.M)) {
+          src[i] = p.X + m * p.ldx + k0 + 8 * unit;
+          vec |= (unsigned)(p.vec_a >> SEEDLM_MAX_SLICES & 1) << i;
+        }
       }
-    } else {
-      const int slot = group * NG + row - kTall, s = slot / p.slots, r = slot - s * p.slots;
-      if (s < p.ad.slices && r < rank) {
-        src[i] = static_cast<const uint16_t*>(p.ad.A[s]) + a * p.ad.a_adapter[s] + r * p.ad.a_row[s];
-        bytes[i] = 16;
-        aligned16 = p.vec_a >> s & 1;
+      there |= (unsigned)(src[i] != nullptr) << i;
+      if (!src[i])
+        for (int st = 0; st < L::kStages; ++st)
+          *reinterpret_cast<uint4*>(smem + st * L::kStageBytes + i * 2048 + place) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    const bool all_vec = vec == there;
+    auto fetch = [&](int step) {
+      if (step < steps) {
+        unsigned char* to = smem + step % L::kStages * L::kStageBytes + place;
+        const int left = k1 - k0 - step * L::kCols - 8 * unit;
+        if (all_vec) {
+          const int bytes = max(0, min(16, 2 * left));
+#pragma unroll
+          for (int i = 0; i < kMine; ++i)
+            if (there >> i & 1) copy16(to + i * 2048, src[i] + step * L::kCols, bytes);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kMine; ++i)
+            if (there >> i & 1)
+              *reinterpret_cast<uint4*>(to + i * 2048) = load8_slow(src[i] + step * L::kCols, 0, left);
+        }
       }
-    }
-    vec |= (unsigned)aligned16 << i;
-    src[i] += bytes[i] ? k0 + 8 * unit : 0;
-  }
-  const bool all_vec = vec == (1u << kMine) - 1;
-  auto fetch = [&](int step) {
-    unsigned char* to = smem + step % kStages * kStageBytes + row0 * 128 + (unit ^ (row0 & 1) * 4) * 16;
-    const int left = k1 - k0 - step * kStageCols - 8 * unit;
-    if (all_vec && left >= 8) {
+      copies_commit();
+    };
+    for (int i = 0; i < L::kStages - 1; ++i) fetch(i);
+    const uint32_t idesc = tc::idesc_f16(kTall, BF16 ? 1 : 0);
+    for (int step = 0; step < steps; ++step) {
+      copies_wait<L::kStages - 2>();
+      tc::fence_proxy_async();
+      __syncthreads();
+      const int st = step % L::kStages;
+      if (warp == 0) {
+        const uint64_t w = tc::smem_desc_sw128(tc::smem_u32(smem + st * L::kStageBytes));
+        const uint64_t x = w + L::kSlots * 128 / 16;
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) copy16(to + i * 4096, src[i], bytes[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int have = bytes[i] ? min(8, left) : 0;
-        if (have <= 0) *reinterpret_cast<uint4*>(to + i * 4096) = make_uint4(0u, 0u, 0u, 0u);
-        else if (vec >> i & 1) copy16(to + i * 4096, src[i], 2 * have);
-        else *reinterpret_cast<uint4*>(to + i * 4096) = load8_slow(src[i], 0, left);
+        for (int k = 0; k < 4; ++k)
+          tc::mma_f16_ss_warp(tmem + step % L::kSums * kTall, w + 2 * k, x + 2 * k, idesc, step >= L::kSums || k > 0);
+        tc::mma_commit_warp(bars + 8 * st);
       }
+      // The stage before this one is read: its place takes the step after next.
+      if (step > 0)
+        ok = tc::mbar_wait_or_abort(bars + 8 * ((step - 1) % L::kStages), ((step - 1) / L::kStages) & 1, kTallWaitLimit,
+                                    slot + 1) && ok;
+      fetch(step + L::kStages - 1);
     }
+    if (steps > 0)
+      ok = tc::mbar_wait_or_abort(bars + 8 * ((steps - 1) % L::kStages), ((steps - 1) / L::kStages) & 1, kTallWaitLimit,
+                                  slot + 1) && ok;
+    tc::fence_after_sync();
+    copies_wait<0>();
+    __syncthreads();  // the stages are read by all: the sums go over them
+    float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) src[i] += kStageCols;
-  };
-  for (int i = 0; i < kStages - 1; ++i) {
-    if (i < steps) fetch(i);
-    copies_commit();
-  }
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
-  const int r0 = warp % WR * RB * 16, t0 = warp / WR * NT * 8;
-  float acc[RB][NT][4] = {};
-  for (int step = 0; step < steps; ++step) {
-    copies_wait<kStages - 2>();
-    __syncthreads();  // the stage is there, and the one before it read by all
-    if (step + kStages - 1 < steps) fetch(step + kStages - 1);
-    copies_commit();
-    const unsigned char* stage = smem + step % kStages * kStageBytes;
-    // The tensor cores cut off what an addition leaves below the sum's last
-    // bit, so they only add up one stage; the stages are added in fp32, rounded.
-    float part_acc[RB][NT][4] = {};
+    for (int c = 0; c < kTall / 16; ++c) {
+      float v[16] = {};
 #pragma unroll
-    for (int c = 0; c < kStageCols / kStep; ++c) {
-      const int at = ((4 * c + q) ^ (g & 1) * 4) * 16;  // rows below differ from g by multiples of 8
-      uint4 w[RB][2];
+      for (int j = 0; j < L::kSums; ++j) {
+        if (j >= steps) break;
+        float d[16];
+        tc::tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + j * kTall + 16 * c, d);
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
+        for (int r = 0; r < 16; ++r) v[r] += d[r];
+      }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          w[b][h] = *reinterpret_cast<const uint4*>(stage + (kTall + r0 + 16 * b + 8 * h + g) * 128 + at);
-      uint4 x[NT];
-#pragma unroll
-      for (int i = 0; i < NT; ++i) x[i] = *reinterpret_cast<const uint4*>(stage + (t0 + 8 * i + g) * 128 + at);
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int b = 0; b < RB; ++b) mma_half<BF16>(half, part_acc[b][i], w[b][0], w[b][1], x[i]);
+      for (int r = 0; r < 16; ++r) sums[(16 * c + r) * L::kSumStride + tid] = v[r];
     }
-#pragma unroll
-    for (int b = 0; b < RB; ++b)
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[b][i][e] += part_acc[b][i][e];
+    store_sums<BF16, L::kSlots>(p, sums, L::kSumStride, first, count, rank, group * L::kSlots,
+                                p.ad.scales ? p.ad.scales[a] : 1.f);
   }
-  copies_wait<0>();
-  __syncthreads();  // the stages are read: the sums go over them
-  float* sums = reinterpret_cast<float*>(smem);
-#pragma unroll
-  for (int b = 0; b < RB; ++b)
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        sums[(t0 + 8 * i + 2 * q + e % 2) * kSumStride + r0 + 16 * b + 8 * (e / 2) + g] = acc[b][i][e];
-  store_sums<BF16, NG>(p, sums, kSumStride, first, count, rank, group * NG, p.ad.scales ? p.ad.scales[a] : 1.f);
+  if (!ok && lane == 0) atomicOr(&g_wait_error, 1u);
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, L::kColumns);
+  }
 }
 
 // ---- the second kernel
@@ -699,11 +726,9 @@ struct ExpandTile {
 
 // False if this CTA has nothing to do.
 __device__ __forceinline__ bool expand_tile(const ApplyArgs& p, int chunks, int in_place, ExpandTile& x) {
-  if (!plan_fits(p)) return false;
-  const int32_t* tail = plan_tail_of(p);
   const int t = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-  if (t >= tail[in_place ? 2 : 3]) return false;
-  const int4 tile = reinterpret_cast<const int4*>(tail)[1 + t];
+  const int4 tile = plan_tile(p, t), head = plan_head(p);
+  if (t >= (in_place ? head.z : head.w)) return false;
   x.a = tile.x;
   x.first = tile.y;
   x.count = tile.z;
@@ -917,9 +942,6 @@ struct TallLayout {
   static constexpr int kBytes = kBars + 8 + 8;              // barrier, tensor memory's address, give-up flag
   static constexpr int kCtas = NB == 1 ? 3 : 1;             // on an SM
 };
-// A product of one tile takes microseconds; a wait this long never ends.
-constexpr uint64_t kTallWaitLimit = 2000000000ull;
-
 template <bool BF16, int NB>
 __global__ void __launch_bounds__(kTallThreads, NB == 1 ? 3 : 1)
 adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int in_place) {
@@ -932,10 +954,6 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
   float* unscale = reinterpret_cast<float*>(smem + L::kScales);
   const uint32_t done = tc::smem_u32(smem + L::kBars);
   volatile uint32_t* slot = reinterpret_cast<uint32_t*>(smem + L::kBars + 8);
-  if (!plan_fits(p)) {
-    grid_wait();
-    return;
-  }
   if (warp == 0) tc::tmem_alloc(tc::smem_u32(smem + L::kBars + 8), L::kColumns);
   if (tid == 32) {
     tc::mbar_init(done, 1);
@@ -950,8 +968,8 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
   grid_launch_dependents();
   const uint32_t tmem = slot[0];
 
-  const int32_t* tail = plan_tail_of(p);
-  const int64_t total = (int64_t)tail[in_place ? 2 : 3] * chunks;
+  const int4 head = plan_head(p);
+  const int64_t total = (int64_t)(in_place ? head.z : head.w) * chunks;
   int64_t item = total * blockIdx.x / gridDim.x;
   const int64_t end = total * (blockIdx.x + 1) / gridDim.x;
   // This thread's units of B and S: 16 bytes `unit` of rows row0, row0 + 16, ...
@@ -961,7 +979,7 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
   bool waited = false, ok = true;
   while (item < end) {
     // The items of one tile and slice.
-    const int4 tile = reinterpret_cast<const int4*>(tail)[1 + item / chunks];
+    const int4 tile = plan_tile(p, item / chunks);
     const int a = tile.x, first = tile.y, count = tile.z;
     const int chunk = (int)(item % chunks);
     int s = 0;
@@ -1056,14 +1074,16 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
       }
       tc::mma_commit_warp(done);
     };
-    // Base of rows 16 q .. 16 q + 15 of item i, two outputs of each.
+    // Base of rows 16 q .. 16 q + 15 of item i, two outputs of each.  Base and Y
+    // pass through L2 as what is first to leave it, so that B stays for the
+    // adapter's other tiles (measured without: B came from memory every time).
     float2 ahead[kQ];
     auto ask = [&](int i, int q) {
       const int n = c0 + i * kOut + 2 * tid;
       const float* from = p.base + n;
       if (pairs && count >= kQ * (q + 1) && c0 + (i + 1) * kOut <= rows) {
 #pragma unroll
-        for (int r = 0; r < kQ; ++r) ahead[r] = __ldcg(reinterpret_cast<const float2*>(from + from_row[kQ * q + r]));
+        for (int r = 0; r < kQ; ++r) ahead[r] = __ldcs(reinterpret_cast<const float2*>(from + from_row[kQ * q + r]));
       } else {
 #pragma unroll
         for (int r = 0; r < kQ; ++r) {
@@ -1115,7 +1135,7 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
         if (!ok) continue;
         if (pairs && count >= kQ * (q + 1) && c0 + (i + 1) * kOut <= rows) {
 #pragma unroll
-          for (int r = 0; r < kQ; ++r) *reinterpret_cast<float2*>(to + to_row[kQ * q + r]) = v[r];
+          for (int r = 0; r < kQ; ++r) __stcs(reinterpret_cast<float2*>(to + to_row[kQ * q + r]), v[r]);
         } else {
 #pragma unroll
           for (int r = 0; r < kQ; ++r) {
@@ -1168,11 +1188,11 @@ int launch_adapters_plan(int M, int n, const int32_t* ids, int32_t* plan, cudaSt
 namespace {
 
 // How the first product is shared out: 16 `blocks` ranks of a slice to a cluster
-// of the low form, `ng` slots of all slices together to one of the tall form;
-// the columns in as many parts (CTAs of a cluster) as fill the GPU when there
+// of the low form, 128 slots of all slices together to one of the tall form; the
+// columns in as many parts (CTAs of a cluster) as fill the GPU when there
 // are few tiles, none so short that its rings are not filled once.
 struct ShrinkShape {
-  int slots, blocks, ng, groups, splits, split_cols;
+  int slots, blocks, groups, splits, split_cols;
 };
 
 ShrinkShape shrink_shape(const seedlm_adapters& ad, int M, const DeviceInfo& dev) {
@@ -1185,16 +1205,15 @@ ShrinkShape shrink_shape(const seedlm_adapters& ad, int M, const DeviceInfo& dev
     clusters *= sh.groups * ad.slices;
     round = kLowWarps * 4;
   } else {
-    const int width = ad.slices * sh.slots;
-    sh.ng = width > 64 ? 128 : width > 32 ? 64 : 32;
-    sh.groups = (width + sh.ng - 1) / sh.ng;
+    sh.groups = (ad.slices * sh.slots + ShrinkTallLayout::kSlots - 1) / ShrinkTallLayout::kSlots;
     clusters *= sh.groups;
-    round = kStages * kStageCols / kStep;
+    round = ShrinkTallLayout::kStages * ShrinkTallLayout::kCols / kStep;
   }
   const int64_t steps = (ad.cols + kStep - 1) / kStep;
   sh.splits = 1;
   while (sh.splits < kMaxSplits && sh.splits * clusters < 3 * dev.num_sms && steps >= 2 * sh.splits * round) sh.splits *= 2;
-  sh.split_cols = (int)((steps + sh.splits - 1) / sh.splits * kStep);
+  // Parts begin at whole stages of either form.
+  sh.split_cols = (int)(((steps + sh.splits - 1) / sh.splits + 1) / 2 * 2 * kStep);
   return sh;
 }
 
@@ -1215,10 +1234,11 @@ int launch_shrink_low(const ApplyArgs& p, int64_t tiles, int splits, cudaStream_
                                 32 * kLowWarps, kShrinkLowSmem<RB>, splits, stream, dev, p);
 }
 
-template <bool BF16, int NG, int WR>
+template <bool BF16>
 int launch_shrink_tall(const ApplyArgs& p, int64_t tiles, int splits, cudaStream_t stream, const DeviceInfo& dev) {
-  return launch_products_kernel(adapters_shrink_tall_kernel<BF16, NG, WR>, tiles * p.groups * splits, kThreads,
-                                kStages * (kTall + NG) * 128, splits, stream, dev, p);
+  using L = ShrinkTallLayout;
+  return launch_products_kernel(adapters_shrink_tall_kernel<BF16>, tiles * p.groups * splits, L::kThreads, L::kBytes,
+                                splits, stream, dev, p);
 }
 
 template <bool BF16, int KC, bool MANY>
@@ -1237,15 +1257,13 @@ int launch_expand_tall(const ApplyArgs& p, int64_t items, int chunks, cudaStream
 
 template <bool BF16>
 int launch_products(ApplyArgs& p, const ShrinkShape& sh, int64_t tiles, cudaStream_t stream, const DeviceInfo& dev) {
-  const bool low = sh.ng == 0;
+  const bool low = adapter_tile_rows(p.M) == 8;
   int rc;
   if (low)
     rc = sh.blocks == 4 ? launch_shrink_low<BF16, 4>(p, tiles, sh.splits, stream, dev)
                         : launch_shrink_low<BF16, 2>(p, tiles, sh.splits, stream, dev);
   else
-    rc = sh.ng == 128  ? launch_shrink_tall<BF16, 128, 4>(p, tiles, sh.splits, stream, dev)
-         : sh.ng == 64 ? launch_shrink_tall<BF16, 64, 4>(p, tiles, sh.splits, stream, dev)
-                       : launch_shrink_tall<BF16, 32, 2>(p, tiles, sh.splits, stream, dev);
+    rc = launch_shrink_tall<BF16>(p, tiles, sh.splits, stream, dev);
   if (rc) return rc;
   // Chunks of outputs.  Low tiles, a CTA each: as long as they can be (a CTA
   // fetches its S once) with enough CTAs left for several rounds of the GPU, at
