@@ -1199,7 +1199,8 @@ ShrinkShape shrink_shape(const seedlm_adapters& ad, int M, const DeviceInfo& dev
   ShrinkShape sh{};
   sh.slots = ad.rank <= 32 ? 32 : (ad.rank + 63) / 64 * 64;
   int64_t clusters = max_tiles(M, ad.n), round;
-  if (adapter_tile_rows(M) == 8) {
+  const bool low = adapter_tile_rows(M) == 8;
+  if (low) {
     sh.blocks = sh.slots == 32 ? 2 : 4;
     sh.groups = sh.slots / (16 * sh.blocks);
     clusters *= sh.groups * ad.slices;
@@ -1209,9 +1210,14 @@ ShrinkShape shrink_shape(const seedlm_adapters& ad, int M, const DeviceInfo& dev
     clusters *= sh.groups;
     round = ShrinkTallLayout::kStages * ShrinkTallLayout::kCols / kStep;
   }
+  // Low: enough CTAs for three on each SM.  Tall: no more than the two that fit
+  // one (a second round of CTAs costs more than their shorter parts save; 4096
+  // rows, 8192 columns: 32 us in one round of 4 parts, 42 in two of 8).
   const int64_t steps = (ad.cols + kStep - 1) / kStep;
   sh.splits = 1;
-  while (sh.splits < kMaxSplits && sh.splits * clusters < 3 * dev.num_sms && steps >= 2 * sh.splits * round) sh.splits *= 2;
+  while (sh.splits < kMaxSplits && steps >= 2 * sh.splits * round &&
+         (low ? sh.splits * clusters < 3 * dev.num_sms : sh.splits * clusters <= dev.num_sms))
+    sh.splits *= 2;
   // Parts begin at whole stages of either form.
   sh.split_cols = (int)(((steps + sh.splits - 1) / sh.splits + 1) / 2 * 2 * kStep);
   return sh;

@@ -367,45 +367,64 @@ def row_bytes(fmt) -> tuple[int, int]:
 
 # ---------------------------------------------- what runs between the products
 
+_CODES: dict = {}  # torch element types by their code in the library
+
+
 def _any_dtype(t) -> int:
-    import torch
-    return F32 if t.dtype == torch.float32 else _act_dtype(t)
+    if not _CODES:
+        import torch
+        _CODES.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"expected float16, bfloat16 or float32, got {t.dtype}")
+    return code
+
+
+def _f32_ld(t, M: int, cols: int, name: str) -> int:
+    if _any_dtype(t) != F32:
+        raise TypeError(f"{name} must be float32, got {t.dtype}")
+    return _rows_ld(t, M, cols, name)
 
 
 def _rows_ld(t, M: int, cols: int, name: str) -> int:
     """Leading dimension of an M x cols argument with unit column stride."""
-    if t.dim() != 2 or t.shape[0] != M or t.shape[1] != cols:
+    if t.shape != (M, cols):
         raise ValueError(f"{name} must be {M} x {cols}, got {tuple(t.shape)}")
     ld, step = t.stride()
-    if cols > 1 and step != 1:
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
     return ld if M > 1 else max(ld, cols)
 
 
-def _is_f32(t, name: str):
-    import torch
-    if t.dtype != torch.float32:
-        raise TypeError(f"{name} must be float32, got {t.dtype}")
-    return t
-
-
-def _run_on(device: int, tensors, stream, fn: str, call):
-    """call(stream) with `device` current; every tensor must live there."""
-    import torch
+def _place(tensors) -> int:
+    """The CUDA device that all of `tensors` (some may be None) are on."""
+    device = None
     for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise ValueError("every tensor of a call must be on the same CUDA device")
-    if device < 0:
+        if t is not None:
+            at = t.get_device()
+            if device is None:
+                device = at
+            elif at != device:
+                raise ValueError("tensors must all be on the same CUDA device")
+    if device is None or device < 0:
         raise ValueError("tensors must be on a CUDA device")
+    return device
+
+
+def _run_on(device: int, stream, fn: str, *args):
+    """The library's `fn` on its arguments and the stream, with `device` current."""
+    import torch
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if not isinstance(stream, int):
+        stream = torch._C._cuda_getCurrentRawStream(device)  # current_stream() makes an object
+    elif not isinstance(stream, int):
         stream = stream.cuda_stream
     if device == torch.cuda.current_device():
-        _check(fn, call(stream))
+        rc = getattr(lib, fn)(*args, stream)
     else:
         with torch.cuda.device(device):
-            _check(fn, call(stream))
+            rc = getattr(lib, fn)(*args, stream)
+    if rc != 0:
+        _check(fn, rc)
 
 
 class Adapters:
@@ -447,6 +466,8 @@ class Adapters:
         self.total_rows = sum(self.rows)
         self.tensors = [*A, *B, ranks, scales]
         self.device = A[0].get_device()
+        if any(v is not None and v.get_device() != self.device for v in self.tensors):
+            raise ValueError("tensors must all be on the same CUDA device")
         s = _AdaptersStruct(n, rank, cols, len(A), _act_dtype(A[0]))
         for i, (a, b) in enumerate(zip(A, B)):
             s.rows[i], s.A[i], s.B[i] = b.shape[1], a.data_ptr(), b.data_ptr()
@@ -487,9 +508,8 @@ def adapter_plan(ids, n: int, plan: AdapterPlan | None = None, stream=None) -> A
         plan = AdapterPlan(M, n, device=ids.device)
     elif plan.M != M or plan.n != n:
         raise ValueError(f"the plan is for {plan.M} rows and {plan.n} adapters, not {M} and {n}")
-    _run_on(ids.get_device(), (plan.buffer,), stream, "seedlm_adapters_plan",
-            lambda st: lib.seedlm_adapters_plan(M, plan.n, ids.data_ptr(), plan.buffer.data_ptr(),
-                                                st))
+    _run_on(_place((ids, plan.buffer)), stream, "seedlm_adapters_plan", M, plan.n, ids.data_ptr(),
+            plan.buffer.data_ptr())
     return plan
 
 
@@ -522,16 +542,16 @@ def adapter_apply(adapters: Adapters, plan: AdapterPlan, X, Y, base=None, worksp
     if plan.n != adapters.n:
         raise ValueError(f"the plan is for {plan.n} adapters, not {adapters.n}")
     ldx = _rows_ld(X, M, adapters.cols, "X")
-    ldy = _rows_ld(_is_f32(Y, "Y"), M, adapters.total_rows, "Y")
-    ldb = ldy if base is None else _rows_ld(_is_f32(base, "base"), M, adapters.total_rows, "base")
+    ldy = _f32_ld(Y, M, adapters.total_rows, "Y")
+    ldb = ldy if base is None else _f32_ld(base, M, adapters.total_rows, "base")
     if workspace is None:
         workspace = adapter_workspace(adapters, M)
-    _run_on(adapters.device, (X, Y, base, plan.buffer, workspace, *adapters.tensors), stream,
-            "seedlm_adapters_apply",
-            lambda st: lib.seedlm_adapters_apply(
-                adapters.ref, plan.buffer.data_ptr(), M, X.data_ptr(), ldx, _ptr(base), ldb,
-                Y.data_ptr(), ldy, workspace.data_ptr(),
-                workspace.numel() * workspace.element_size(), st))
+    device = _place((X, Y, base, plan.buffer, workspace))
+    if device != adapters.device:
+        raise ValueError("tensors must all be on the same CUDA device")
+    _run_on(device, stream, "seedlm_adapters_apply", adapters.ref, plan.buffer.data_ptr(), M,
+            X.data_ptr(), ldx, None if base is None else base.data_ptr(), ldb, Y.data_ptr(), ldy,
+            workspace.data_ptr(), workspace.nbytes)
 
 
 class BlockNorm:
@@ -557,6 +577,7 @@ class BlockNorm:
             _dense(t, "a weight or bias")
         self.cols = int(cols)
         self.tensors = given
+        self.device = _place(given) if any(t.get_device() >= 0 for t in given) else None
         post = w_post is not None or b_post is not None if post is None else bool(post)
         self.struct = _NormStruct(
             self.cols, 1 if kind == "layer" else 0, _any_dtype(torch.empty(0, dtype=self.dtype)),
@@ -575,18 +596,20 @@ def block_norm(norm: BlockNorm, y, h, h_out=None, x=None, gate=None, stream=None
     if like is None or (h_out is None and x is None):
         raise ValueError("y or h, and h_out or x, must be given")
     M, cols = like.shape[0] if like.dim() else 0, norm.cols
-    ldy = ldg = ldh = ldo = ldx = 0
+    ldy = ldg = ldh = ldo = ldx = ht = xt = 0
+    py = pg = ph = po = px = None
     if y is not None:
-        ldy = _rows_ld(_is_f32(y, "y"), M, cols, "y")
-    ht = xt = 0
+        ldy, py = _f32_ld(y, M, cols, "y"), y.data_ptr()
     if h is not None:
-        ldh, ht = _rows_ld(h, M, cols, "h"), _any_dtype(h)
+        ldh, ph, ht = _rows_ld(h, M, cols, "h"), h.data_ptr(), _any_dtype(h)
     if h_out is not None:
-        ldo, ht = _rows_ld(h_out, M, cols, "h_out"), _any_dtype(h_out)
         if h is not None and h.dtype != h_out.dtype:
             raise TypeError("h and h_out must have one element type")
+        ldo, po, ht = _rows_ld(h_out, M, cols, "h_out"), h_out.data_ptr(), _any_dtype(h_out)
     if x is not None:
-        ldx, xt = _rows_ld(x, M, cols, "x"), _act_dtype(x)
+        ldx, px, xt = _rows_ld(x, M, cols, "x"), x.data_ptr(), _any_dtype(x)
+        if xt == F32:
+            raise TypeError("x must be float16 or bfloat16, got float32")
     if gate is not None:
         if gate.dtype != norm.dtype:
             raise TypeError(f"gate must be {norm.dtype} as the norm's parameters are")
@@ -596,9 +619,12 @@ def block_norm(norm: BlockNorm, y, h, h_out=None, x=None, gate=None, stream=None
             _dense(gate, "gate")
         else:
             ldg = _rows_ld(gate, M, cols, "gate")
-    _run_on(like.get_device(), (y, h, h_out, x, gate, *norm.tensors), stream, "seedlm_block_norm",
-            lambda st: lib.seedlm_block_norm(norm.ref, M, _ptr(y), ldy, _ptr(gate), ldg, _ptr(h),
-                                             ldh, _ptr(h_out), ldo, ht, _ptr(x), ldx, xt, st))
+        pg = gate.data_ptr()
+    device = _place((y, h, h_out, x, gate))
+    if norm.device is not None and device != norm.device or norm.device is None and norm.tensors:
+        raise ValueError("tensors must all be on the same CUDA device")
+    _run_on(device, stream, "seedlm_block_norm", norm.ref, M, py, ldy, pg, ldg, ph, ldh, po, ldo,
+            ht, px, ldx, xt)
 
 
 #: Activations of glu().
@@ -614,7 +640,6 @@ def glu(GU, X, act: str = "silu", stream=None):
         raise ValueError("X must be M x cols")
     M, cols = X.shape
     ldx, xt = _rows_ld(X, M, cols, "X"), _act_dtype(X)
-    ldgu = _rows_ld(_is_f32(GU, "GU"), M, 2 * cols, "GU")
-    _run_on(X.get_device(), (GU,), stream, "seedlm_glu",
-            lambda st: lib.seedlm_glu(M, cols, ACTIVATIONS[act], GU.data_ptr(), ldgu, X.data_ptr(),
-                                      ldx, xt, st))
+    ldgu = _f32_ld(GU, M, 2 * cols, "GU")
+    _run_on(_place((X, GU)), stream, "seedlm_glu", M, cols, ACTIVATIONS[act], GU.data_ptr(), ldgu,
+            X.data_ptr(), ldx, xt)

@@ -413,6 +413,12 @@ def test_a_workspace_that_is_too_small_or_misaligned_is_refused(gpu):
             gpu.adapter_apply(ad, plan, d["X"], Y, workspace=bad)
     with pytest.raises(ValueError, match="same CUDA device"):
         gpu.adapter_apply(ad, plan, d["X"], torch.empty(20, 32), workspace=ws)
+    with pytest.raises(ValueError, match="same CUDA device"):
+        gpu.adapter_apply(ad, plan, d["X"].cpu(), Y, workspace=ws)
+    with pytest.raises(ValueError, match="same CUDA device"):
+        gpu.adapter_plan(d["ids"].cpu(), 4, plan=plan)
+    with pytest.raises(ValueError, match="same CUDA device"):
+        gpu.Adapters(d["A"][0].cpu(), d["B"])
     torch.cuda.synchronize()
     assert bool((Y == 7.0).all())
 
