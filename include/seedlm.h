@@ -281,7 +281,7 @@ SEEDLM_API uint32_t seedlm_lfsr_taps(int32_t K);
  * A[s] + a * a_adapter[s], row r at + r * a_row[s]; B_{s,a} is rows[s] x rank
  * at B[s] + a * b_adapter[s], row j at + j * b_row[s].  Adapter a uses the
  * first ranks[a] rows of A and columns of B (clamped to 0..rank; what lies
- * beyond is never read); ranks == NULL: all use `rank`.  scales == NULL: 1. */
+ * beyond has no effect); ranks == NULL: all use `rank`.  scales == NULL: 1. */
 enum { SEEDLM_MAX_SLICES = 4, SEEDLM_MAX_RANK = 256, SEEDLM_MAX_ADAPTERS = 1024 };
 
 typedef struct seedlm_adapters {
@@ -323,9 +323,8 @@ SEEDLM_API int64_t seedlm_adapters_plan_words(int32_t M, int32_t n);
  * made for others changes nothing in Y and sets value 4 of
  * seedlm_device_error.  Sums are fp32 in a fixed order per shape; x A^T is
  * kept to 24 bits between the two products.  Any alignment of X, A, B, base
- * and Y that their types allow is accepted; 16-byte aligned arrays with
- * strides and row counts that keep every row aligned are read 16 bytes at a
- * time.  `workspace`: device memory of at least
+ * and Y that their types allow is accepted; arrays whose rows all begin at
+ * multiples of 16 bytes are read fastest.  `workspace`: device memory of at least
  * seedlm_adapters_workspace_bytes(ad, M) bytes, 256-byte aligned, of any
  * content; calls that share one must not run concurrently (calls on one
  * stream never do). */

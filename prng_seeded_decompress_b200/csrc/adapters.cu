@@ -265,9 +265,8 @@ struct ApplyArgs {
   int chunk_first[SEEDLM_MAX_SLICES + 1];  // second kernel: chunks of outputs before each slice
   int chunk_rows;   // outputs of a chunk
   int slice_at[SEEDLM_MAX_SLICES];         // first output of each slice
-  int vec_a, vec_b, vec_y;  // rows can be read 16 bytes at a time: bit s for slice s, bit
-                            // SEEDLM_MAX_SLICES of vec_a for X
-  int pair_y;               // base and Y 8 bytes at a time
+  // Bytes that every row's address is a multiple of, at most 16.
+  int grain_x, grain_a[SEEDLM_MAX_SLICES], grain_b[SEEDLM_MAX_SLICES], grain_y[SEEDLM_MAX_SLICES];
 };
 
 __device__ __forceinline__ const int32_t* plan_tail_of(const ApplyArgs& p) { return p.plan + plan_tail(p.M, p.ad.n); }
@@ -292,15 +291,6 @@ __device__ __forceinline__ int4 plan_tile(const ApplyArgs& p, int64_t t) {
 __device__ __forceinline__ int rank_of(const seedlm_adapters& ad, int a) {
   if (a < 0) return 0;
   return ad.ranks ? max(0, min(ad.ranks[a], ad.rank)) : ad.rank;
-}
-
-// Elements k .. k + 7 of a row of `len`, zero beyond its end, one at a time.
-__device__ __forceinline__ uint4 load8_slow(const uint16_t* row, int k, int len) {
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (k + i < len) w[i / 2] |= (uint32_t)__ldg(row + k + i) << (16 * (i % 2));
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <bool BF16>
@@ -344,6 +334,105 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int LEFT>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+template <int SIZE>
+__device__ __forceinline__ void copy_small(void* to, const void* from, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+               "n"(SIZE), "r"(bytes)
+               : "memory");
+}
+
+// Eight elements of a row on their way to a 16-byte unit of shared memory: the
+// first `have` are wanted (0..8), the others become zeros.  before, after: how
+// many elements there are to read before `from` and from it on, in the matrix.
+struct Unit {
+  unsigned char* to;
+  const uint16_t* from;
+  int have;
+  int64_t before, after;
+};
+
+// A unit of a row that is only aligned to its elements: the two 16-byte words
+// that it lies across, shifted together; where one of them would leave the
+// matrix, element by element.
+__device__ __forceinline__ uint4 load_unit(const Unit& u) {
+  if (u.have <= 0) return make_uint4(0u, 0u, 0u, 0u);
+  const int off = (int)(reinterpret_cast<uintptr_t>(u.from) & 15) / 2;
+  uint4 v;
+  if (u.before >= off && u.after >= 16 - off) {
+    const uint4* at = reinterpret_cast<const uint4*>(u.from - off);
+    const uint4 lo = __ldg(at), hi = __ldg(at + (off ? 1 : 0));
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = off & 4 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = off & 2 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16 * (off & 1));
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i)
+      if (i < u.have) {
+        const uint32_t e = (uint32_t)__ldg(u.from + i) << (16 * (i % 2));
+        if (i < 2) w[0] |= e;
+        else if (i < 4) w[1] |= e;
+        else if (i < 6) w[2] |= e;
+        else w[3] |= e;
+      }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  const uint32_t odd = u.have & 1 ? 0x0000ffffu : 0xffffffffu;  // of the word the row ends in
+  const int words = (u.have + 1) / 2;
+  v.x &= words == 1 ? odd : 0xffffffffu;
+  v.y &= words == 2 ? odd : words < 2 ? 0u : 0xffffffffu;
+  v.z &= words == 3 ? odd : words < 3 ? 0u : 0xffffffffu;
+  v.w &= words == 4 ? odd : words < 4 ? 0u : 0xffffffffu;
+  return v;
+}
+
+// Units 0 .. N - 1 of rows whose addresses are multiples of `grain` bytes (16, 8,
+// 4 or 2): asynchronous copies of that size, of rows of odd elements loads, four
+// units' together.  SHORT: see copy16_short.  WIDE: the grain is known to be 16
+// (the kernels are built with and without, for the checks of the others cost
+// the common case up to 15 %).
+template <int N, bool SHORT, bool WIDE, class F>
+__device__ __forceinline__ void copy_units(int grain, F unit) {
+  if (WIDE || grain == 16) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const Unit u = unit(i);
+      if (SHORT) copy16_short(u.to, u.from, 2 * u.have);
+      else copy16(u.to, u.from, 2 * u.have);
+    }
+  } else if (grain == 8) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const Unit u = unit(i);
+#pragma unroll
+      for (int o = 0; o < 8; o += 4) copy_small<8>(u.to + 2 * o, u.from + o, max(0, min(8, 2 * (u.have - o))));
+    }
+  } else if (grain == 4) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const Unit u = unit(i);
+#pragma unroll
+      for (int o = 0; o < 8; o += 2) copy_small<4>(u.to + 2 * o, u.from + o, max(0, min(4, 2 * (u.have - o))));
+    }
+  } else {
+#pragma unroll
+    for (int i0 = 0; i0 < N; i0 += 4) {
+      uint4 v[4];
+#pragma unroll
+      for (int i = i0; i < i0 + 4; ++i)
+        if (i < N) v[i - i0] = load_unit(unit(i));
+#pragma unroll
+      for (int i = i0; i < i0 + 4; ++i)
+        if (i < N) *reinterpret_cast<uint4*>(unit(i).to) = v[i - i0];
+    }
+  }
 }
 
 // ---- the first kernel's end: the cluster's sums to S
@@ -438,7 +527,7 @@ constexpr int kShrinkLowStages = RB == 4 ? 4 : 6;
 template <int RB>
 constexpr int kShrinkLowSmem = kLowWarps * kShrinkLowStages<RB> * (2 * RB + 1) * 512;
 
-template <bool BF16, int RB>
+template <bool BF16, int RB, bool WIDE>
 __global__ void __launch_bounds__(32 * kLowWarps)
 adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -458,7 +547,6 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
   const float scale = p.ad.scales ? p.ad.scales[a] : 1.f;
   if (rank <= 0) return;
   const int k0 = (int)cluster_rank() * p.split_cols, k1 = min(p.ad.cols, k0 + p.split_cols);
-  const bool vec = (p.vec_a >> s) & (p.vec_a >> SEEDLM_MAX_SLICES) & 1;
   const int blocks = min(RB, (rank + 15) / 16);
 
   // Row g of the tile and rows 8 j + g of A, at this lane's place in the part.
@@ -471,31 +559,26 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
   const int steps = k1 > k0 ? max(0, ((k1 - k0 + kStep - 1) / kStep - warp + kLowWarps - 1) / kLowWarps) : 0;
   // Every copy of a step is made, those of rows that are not there with no
   // bytes read and zeros written, so what is multiplied below needs no checks.
-  int left = k1 - k_first, fetched = 0;
+  int k = k_first, fetched = 0;
   unsigned char* to = ring;
   auto fetch = [&]() {
     if (fetched < steps) {
-      if (vec) {
-        const int have = max(0, min(16, 2 * left));
+      const int have = max(0, min(8, k1 - k));
 #pragma unroll
-        for (int b = 0; b < RB; ++b)
-          if (b < blocks) {
-#pragma unroll
-            for (int j = 2 * b; j < 2 * b + 2; ++j) {
-              const int r = 8 * j + g;
-              copy16(to + j * 512, A + (r < rank ? r : 0) * a_row, r < rank ? have : 0);
-            }
-          }
-        copy16(to + 2 * RB * 512, x, have_x ? have : 0);
-      } else {
-#pragma unroll 1
-        for (int j = 0; j < 2 * blocks; ++j)
-          *reinterpret_cast<uint4*>(to + j * 512) = load8_slow(A + (8 * j + g) * a_row, 0, 8 * j + g < rank ? left : 0);
-        *reinterpret_cast<uint4*>(to + 2 * RB * 512) = load8_slow(x, 0, have_x ? left : 0);
-      }
+      for (int b = 0; b < RB; ++b)
+        if (b < blocks)
+          copy_units<2, false, WIDE>(p.grain_a[s], [&](int i) {
+            const int r = 16 * b + 8 * i + g;
+            const bool in = r < rank;
+            return Unit{to + (2 * b + i) * 512, A + (in ? r : 0) * a_row, in ? have : 0, r * a_row + k,
+                        (rank - 1 - r) * a_row + p.ad.cols - k};
+          });
+      copy_units<1, false, WIDE>(p.grain_x, [&](int) {
+        return Unit{to + 2 * RB * 512, x, have_x ? have : 0, row * p.ldx + k, (p.M - 1 - row) * p.ldx + p.ad.cols - k};
+      });
       A += kLowWarps * kStep;
       x += kLowWarps * kStep;
-      left -= kLowWarps * kStep;
+      k += kLowWarps * kStep;
       to = to == ring + (kStages - 1) * kStageBytes ? ring : to + kStageBytes;
       ++fetched;
     }
@@ -561,7 +644,7 @@ struct ShrinkTallLayout {
 // A product of one tile takes microseconds; a wait this long never ends.
 constexpr uint64_t kTallWaitLimit = 2000000000ull;
 
-template <bool BF16>
+template <bool BF16, bool WIDE>
 __global__ void __launch_bounds__(ShrinkTallLayout::kThreads, 2)
 adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
   using L = ShrinkTallLayout;
@@ -601,44 +684,56 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
     const int unit = tid % 8, row0 = tid / 8;
     const int place = row0 * 128 + (unit ^ (row0 & 7)) * 16;
     const uint16_t* src[kMine];
-    unsigned there = 0, vec = 0;
+    unsigned there = 0;
+    int grain = 16;  // of all that the CTA copies
+    for (int s = 0; s < p.ad.slices; ++s) grain = min(grain, p.grain_a[s]);
+    grain = min(grain, p.grain_x);
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       const int row = row0 + 16 * i;
       src[i] = nullptr;
       if (row < L::kSlots) {
         const int place_of = group * L::kSlots + row, s = place_of / p.slots, r = place_of - s * p.slots;
-        if (s < p.ad.slices && r < rank) {
-          src[i] = static_cast<const uint16_t*>(p.ad.A[s]) + a * p.ad.a_adapter[s] + r * p.ad.a_row[s] + k0 + 8 * unit;
-          vec |= (unsigned)(p.vec_a >> s & 1) << i;
-        }
+        if (s < p.ad.slices && r < rank)
+          src[i] = static_cast<const uint16_t*>(p.ad.A[s]) + a * p.ad.a_adapter[s] + r * p.ad.a_row[s];
       } else {
         const int m = row - L::kSlots < count ? p.plan[first + row - L::kSlots] : -1;
-        if (m >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, m, p.M)) {
-          src[i] = p.X + m * p.ldx + k0 + 8 * unit;
-          vec |= (unsigned)(p.vec_a >> SEEDLM_MAX_SLICES & 1) << i;
-        }
+        if (m >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, m, p.M)) src[i] = p.X + m * p.ldx;
       }
       there |= (unsigned)(src[i] != nullptr) << i;
       if (!src[i])
         for (int st = 0; st < L::kStages; ++st)
           *reinterpret_cast<uint4*>(smem + st * L::kStageBytes + i * 2048 + place) = make_uint4(0u, 0u, 0u, 0u);
     }
-    const bool all_vec = vec == there;
+    auto unit_of = [&](int i, int step) {
+      const int k = k0 + step * L::kCols + 8 * unit;
+      const bool in = there >> i & 1;
+      // Within the row: its neighbours are not always ones of the same matrix.
+      return Unit{smem + step % L::kStages * L::kStageBytes + place + i * 2048, in ? src[i] + k : p.X,
+                  in ? max(0, min(8, k1 - k)) : 0, k, p.ad.cols - k};
+    };
+    // Rows of odd elements wait in registers from one step to the next.
+    uint4 late[WIDE ? 1 : kMine];
+    int late_step = steps;
     auto fetch = [&](int step) {
+      if (!WIDE && late_step < steps) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) *reinterpret_cast<uint4*>(unit_of(i, late_step).to) = late[WIDE ? 0 : i];
+        late_step = steps;
+      }
       if (step < steps) {
-        unsigned char* to = smem + step % L::kStages * L::kStageBytes + place;
-        const int left = k1 - k0 - step * L::kCols - 8 * unit;
-        if (all_vec) {
-          const int bytes = max(0, min(16, 2 * left));
+        if (WIDE) {
+          unsigned char* to = smem + step % L::kStages * L::kStageBytes + place;
+          const int k = k0 + step * L::kCols + 8 * unit, bytes = max(0, min(16, 2 * (k1 - k)));
 #pragma unroll
           for (int i = 0; i < kMine; ++i)
-            if (there >> i & 1) copy16(to + i * 2048, src[i] + step * L::kCols, bytes);
+            if (there >> i & 1) copy16(to + i * 2048, src[i] + k, bytes);
+        } else if (grain > 2) {
+          copy_units<kMine, false, false>(grain, [&](int i) { return unit_of(i, step); });
         } else {
 #pragma unroll
-          for (int i = 0; i < kMine; ++i)
-            if (there >> i & 1)
-              *reinterpret_cast<uint4*>(to + i * 2048) = load8_slow(src[i] + step * L::kCols, 0, left);
+          for (int i = 0; i < kMine; ++i) late[WIDE ? 0 : i] = load_unit(unit_of(i, step));
+          late_step = step;
         }
       }
       copies_commit();
@@ -752,7 +847,7 @@ constexpr int kLowItemBytes = 2048 * KC + 1024;
 template <int KC>
 constexpr int kExpandLowSmem = kLowWarps * kLowStages * kLowItemBytes<KC>;
 
-template <bool BF16, int KC, bool MANY>
+template <bool BF16, int KC, bool MANY, bool WIDE>
 __global__ void __launch_bounds__(32 * kLowWarps)
 adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int in_place) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -767,7 +862,7 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
   unsigned char* ring = smem + warp * kLowStages * kItemBytes + lane * 16;
   const uint16_t* B = static_cast<const uint16_t*>(p.ad.B[x.s]) + max(x.a, 0) * p.ad.b_adapter[x.s];
   const int64_t b_row = p.ad.b_row[x.s];
-  const bool vec_b = (p.vec_b >> x.s) & 1, vec_y = (p.vec_y >> x.s) & 1;
+  const bool vec_y = p.grain_y[x.s] == 16;
   const float* from[2];
   float* to[2];
 #pragma unroll
@@ -788,29 +883,23 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
   int have[KC];
   auto sizes = [&]() {
 #pragma unroll
-    for (int c = 0; c < KC; ++c) have[c] = max(0, min(16, 2 * (x.rank - fetch_k - kStep * c - 8 * q)));
+    for (int c = 0; c < KC; ++c) have[c] = max(0, min(8, x.rank - fetch_k - kStep * c - 8 * q));
   };
   sizes();
   auto fetch = [&]() {
     if (fetched < items) {
       const bool whole = fetch_n + 32 <= x.c1;
       if (MANY) sizes();
-      if (vec_b && whole) {
-        const uint16_t* b = b_next;
+      const uint16_t* b = b_next;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-#pragma unroll
-          for (int c = 0; c < KC; ++c) copy16_short(into + (4 * c + j) * 512, b + kStep * c, have[c]);
-          b += b_row;
-        }
-      } else {
-#pragma unroll 1
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int c = 0; c < KC; ++c)
-            *reinterpret_cast<uint4*>(into + (4 * c + j) * 512) =
-                load8_slow(b_next + j * b_row + kStep * c, 0,
-                           fetch_n + 4 * g + j < x.c1 ? x.rank - fetch_k - kStep * c - 8 * q : 0);
+      for (int j = 0; j < 4; ++j) {
+        const int n = fetch_n + 4 * g + j;
+        copy_units<KC, true, WIDE>(p.grain_b[x.s], [&](int c) {
+          return Unit{into + (4 * c + j) * 512, b + kStep * c, whole || n < x.c1 ? have[c] : 0,
+                      n * b_row + fetch_k + kStep * c + 8 * q,
+                      (p.ad.rows[x.s] - 1 - n) * b_row + x.rank - fetch_k - kStep * c - 8 * q};
+        });
+        b += b_row;
       }
       b_next += 64;
       fetch_k += 64;
@@ -942,7 +1031,7 @@ struct TallLayout {
   static constexpr int kBytes = kBars + 8 + 8;              // barrier, tensor memory's address, give-up flag
   static constexpr int kCtas = NB == 1 ? 3 : 1;             // on an SM
 };
-template <bool BF16, int NB>
+template <bool BF16, int NB, bool WIDE>
 __global__ void __launch_bounds__(kTallThreads, NB == 1 ? 3 : 1)
 adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int in_place) {
   using L = TallLayout<BF16, NB>;
@@ -991,7 +1080,7 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
     const int rows = p.ad.rows[s], c0 = (chunk - p.chunk_first[s]) * kOut;
     const uint16_t* B = static_cast<const uint16_t*>(p.ad.B[s]) + max(a, 0) * p.ad.b_adapter[s];
     const int64_t b_row = p.ad.b_row[s];
-    const bool vec_b = (p.vec_b >> s) & 1, pairs = (p.pair_y >> s) & 1;
+    const bool pairs = p.grain_y[s] >= 8;
     const bool products = rank > 0;
     __syncthreads();  // the tile before is done with shared memory
     if (tid < T) {
@@ -1007,21 +1096,13 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
       unsigned char* to = smem + L::kB + place;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const int left = rank - 64 * b - 8 * unit;
-        if (vec_b) {
-          const int bytes = max(0, min(16, 2 * left));
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              copy16_short(to + (h * NB + b) * 128 * 128 + j * 16 * 128, src + 64 * b + (32 * j + h) * b_row,
-                           n + 32 * j + h < rows ? bytes : 0);
-        } else {
-#pragma unroll 1
-          for (int j = 0; j < 16; ++j)
-            *reinterpret_cast<uint4*>(to + (j % 2 * NB + b) * 128 * 128 + j / 2 * 16 * 128) =
-                load8_slow(src + 64 * b + (32 * (j / 2) + j % 2) * b_row, 0, n + 32 * (j / 2) + j % 2 < rows ? left : 0);
-        }
+        const int have = max(0, min(8, rank - 64 * b - 8 * unit));
+        copy_units<16, true, WIDE>(p.grain_b[s], [&](int u) {
+          const int j = u / 2, h = u % 2, at = n + 32 * j + h;
+          return Unit{to + (h * NB + b) * 128 * 128 + j * 16 * 128, src + 64 * b + (32 * j + h) * b_row,
+                      at < rows ? have : 0, at * b_row + 64 * b + 8 * unit,
+                      (rows - 1 - at) * b_row + rank - 64 * b - 8 * unit};
+        });
       }
       copies_commit();
     };
@@ -1223,8 +1304,11 @@ ShrinkShape shrink_shape(const seedlm_adapters& ad, int M, const DeviceInfo& dev
   return sh;
 }
 
-bool rows_aligned(const void* p, int64_t ld1, int64_t ld2, int bytes) {
-  return aligned(p, 16) && ld1 * bytes % 16 == 0 && ld2 * bytes % 16 == 0;
+// The largest of 16, 8, 4 .. bytes that the address and the strides are
+// multiples of.
+int grain_of(const void* p, int64_t stride1, int64_t stride2) {
+  const uint64_t all = reinterpret_cast<uintptr_t>(p) | (uint64_t)stride1 | (uint64_t)stride2 | 16;
+  return (int)(all & (0 - all));
 }
 
 template <class Kernel, class... Args>
@@ -1234,42 +1318,42 @@ int launch_products_kernel(Kernel kernel, int64_t grid, int threads, int smem, i
   return rc ? rc : launch_pdl_cluster(kernel, (unsigned)grid, threads, (size_t)smem, cluster, stream, args...);
 }
 
-template <bool BF16, int RB>
+template <bool BF16, bool WIDE, int RB>
 int launch_shrink_low(const ApplyArgs& p, int64_t tiles, int splits, cudaStream_t stream, const DeviceInfo& dev) {
-  return launch_products_kernel(adapters_shrink_low_kernel<BF16, RB>, tiles * p.ad.slices * p.groups * splits,
+  return launch_products_kernel(adapters_shrink_low_kernel<BF16, RB, WIDE>, tiles * p.ad.slices * p.groups * splits,
                                 32 * kLowWarps, kShrinkLowSmem<RB>, splits, stream, dev, p);
 }
 
-template <bool BF16>
+template <bool BF16, bool WIDE>
 int launch_shrink_tall(const ApplyArgs& p, int64_t tiles, int splits, cudaStream_t stream, const DeviceInfo& dev) {
   using L = ShrinkTallLayout;
-  return launch_products_kernel(adapters_shrink_tall_kernel<BF16>, tiles * p.groups * splits, L::kThreads, L::kBytes,
+  return launch_products_kernel(adapters_shrink_tall_kernel<BF16, WIDE>, tiles * p.groups * splits, L::kThreads, L::kBytes,
                                 splits, stream, dev, p);
 }
 
-template <bool BF16, int KC, bool MANY>
+template <bool BF16, bool WIDE, int KC, bool MANY>
 int launch_expand_low(const ApplyArgs& p, int64_t grid, int chunks, cudaStream_t stream, const DeviceInfo& dev) {
-  return launch_products_kernel(adapters_expand_low_kernel<BF16, KC, MANY>, grid, 32 * kLowWarps, kExpandLowSmem<KC>, 1,
+  return launch_products_kernel(adapters_expand_low_kernel<BF16, KC, MANY, WIDE>, grid, 32 * kLowWarps, kExpandLowSmem<KC>, 1,
                                 stream, dev, p, chunks, (int)(p.base == p.Y));
 }
 
-template <bool BF16, int NB>
+template <bool BF16, bool WIDE, int NB>
 int launch_expand_tall(const ApplyArgs& p, int64_t items, int chunks, cudaStream_t stream, const DeviceInfo& dev) {
   using L = TallLayout<BF16, NB>;
-  return launch_products_kernel(adapters_expand_tall_kernel<BF16, NB>,
+  return launch_products_kernel(adapters_expand_tall_kernel<BF16, NB, WIDE>,
                                 std::min(items, (int64_t)L::kCtas * dev.num_sms), kTallThreads, L::kBytes, 1, stream,
                                 dev, p, chunks, (int)(p.base == p.Y));
 }
 
-template <bool BF16>
+template <bool BF16, bool WIDE>
 int launch_products(ApplyArgs& p, const ShrinkShape& sh, int64_t tiles, cudaStream_t stream, const DeviceInfo& dev) {
   const bool low = adapter_tile_rows(p.M) == 8;
   int rc;
   if (low)
-    rc = sh.blocks == 4 ? launch_shrink_low<BF16, 4>(p, tiles, sh.splits, stream, dev)
-                        : launch_shrink_low<BF16, 2>(p, tiles, sh.splits, stream, dev);
+    rc = sh.blocks == 4 ? launch_shrink_low<BF16, WIDE, 4>(p, tiles, sh.splits, stream, dev)
+                        : launch_shrink_low<BF16, WIDE, 2>(p, tiles, sh.splits, stream, dev);
   else
-    rc = launch_shrink_tall<BF16>(p, tiles, sh.splits, stream, dev);
+    rc = launch_shrink_tall<BF16, WIDE>(p, tiles, sh.splits, stream, dev);
   if (rc) return rc;
   // Chunks of outputs.  Low tiles, a CTA each: as long as they can be (a CTA
   // fetches its S once) with enough CTAs left for several rounds of the GPU, at
@@ -1294,12 +1378,12 @@ int launch_products(ApplyArgs& p, const ShrinkShape& sh, int64_t tiles, cudaStre
   const int64_t grid = chunks * tiles;
   if (grid > INT32_MAX) return SEEDLM_EUNSUPPORTED;
   if (low)
-    return p.slots == 32   ? launch_expand_low<BF16, 1, false>(p, grid, (int)chunks, stream, dev)
-           : p.slots == 64 ? launch_expand_low<BF16, 2, false>(p, grid, (int)chunks, stream, dev)
-                           : launch_expand_low<BF16, 2, true>(p, grid, (int)chunks, stream, dev);
-  return p.blocks == 1   ? launch_expand_tall<BF16, 1>(p, grid, (int)chunks, stream, dev)
-         : p.blocks == 2 ? launch_expand_tall<BF16, 2>(p, grid, (int)chunks, stream, dev)
-                         : launch_expand_tall<BF16, 4>(p, grid, (int)chunks, stream, dev);
+    return p.slots == 32   ? launch_expand_low<BF16, WIDE, 1, false>(p, grid, (int)chunks, stream, dev)
+           : p.slots == 64 ? launch_expand_low<BF16, WIDE, 2, false>(p, grid, (int)chunks, stream, dev)
+                           : launch_expand_low<BF16, WIDE, 2, true>(p, grid, (int)chunks, stream, dev);
+  return p.blocks == 1   ? launch_expand_tall<BF16, WIDE, 1>(p, grid, (int)chunks, stream, dev)
+         : p.blocks == 2 ? launch_expand_tall<BF16, WIDE, 2>(p, grid, (int)chunks, stream, dev)
+                         : launch_expand_tall<BF16, WIDE, 4>(p, grid, (int)chunks, stream, dev);
 }
 
 // Bytes of S, then those of its factors.
@@ -1338,17 +1422,21 @@ int launch_adapters_apply(const seedlm_adapters& ad, const int32_t* plan, int M,
   p.groups = sh.groups;
   int64_t at = 0;
   for (int s = 0; s < ad.slices; ++s) {
-    p.vec_a |= rows_aligned(ad.A[s], ad.a_adapter[s], ad.a_row[s], 2) << s;
-    p.vec_b |= rows_aligned(ad.B[s], ad.b_adapter[s], ad.b_row[s], 2) << s;
-    p.vec_y |= (rows_aligned(base, ldb, at, 4) && rows_aligned(Y, ldy, at, 4)) << s;
-    p.pair_y |= (aligned(base, 8) && aligned(Y, 8) && (ldb | ldy | at) % 2 == 0) << s;
+    p.grain_a[s] = grain_of(ad.A[s], 2 * ad.a_adapter[s], 2 * ad.a_row[s]);
+    p.grain_b[s] = grain_of(ad.B[s], 2 * ad.b_adapter[s], 2 * ad.b_row[s]);
+    p.grain_y[s] = std::min(grain_of(base + at, 4 * ldb, 0), grain_of(Y + at, 4 * ldy, 0));
     at += ad.rows[s];
   }
-  p.vec_a |= rows_aligned(X, ldx, 0, 2) << SEEDLM_MAX_SLICES;
+  p.grain_x = grain_of(X, 2 * ldx, 0);
   const int64_t tiles = max_tiles(M, ad.n);
   if (tiles * ad.slices * sh.groups * sh.splits > INT32_MAX) return SEEDLM_EUNSUPPORTED;
-  return ad.dtype == SEEDLM_BF16 ? launch_products<true>(p, sh, tiles, stream, dev)
-                                 : launch_products<false>(p, sh, tiles, stream, dev);
+  bool wide = p.grain_x == 16;
+  for (int s = 0; s < ad.slices; ++s) wide = wide && p.grain_a[s] == 16 && p.grain_b[s] == 16;
+  if (ad.dtype == SEEDLM_BF16)
+    return wide ? launch_products<true, true>(p, sh, tiles, stream, dev)
+                : launch_products<true, false>(p, sh, tiles, stream, dev);
+  return wide ? launch_products<false, true>(p, sh, tiles, stream, dev)
+              : launch_products<false, false>(p, sh, tiles, stream, dev);
 }
 
 int read_and_clear_plan_mismatch(unsigned int* out) {
