@@ -353,86 +353,63 @@ struct Unit {
   int64_t before, after;
 };
 
-// A unit of a row that is only aligned to its elements: the two 16-byte words
-// that it lies across, shifted together; where one of them would leave the
-// matrix, element by element.
-__device__ __forceinline__ uint4 load_unit(const Unit& u) {
-  if (u.have <= 0) return make_uint4(0u, 0u, 0u, 0u);
-  const int off = (int)(reinterpret_cast<uintptr_t>(u.from) & 15) / 2;
-  uint4 v;
-  if (u.before >= off && u.after >= 16 - off) {
-    const uint4* at = reinterpret_cast<const uint4*>(u.from - off);
-    const uint4 lo = __ldg(at), hi = __ldg(at + (off ? 1 : 0));
-    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+__device__ __forceinline__ int off_of(const uint16_t* p) { return (int)(reinterpret_cast<uintptr_t>(p) & 15) / 2; }
+
+// Elements off .. off + 7 of the two neighbouring 16-byte words, the first `have`
+// of them.
+__device__ __forceinline__ uint4 shift_unit(const uint4& lo, const uint4& hi, int off, int have) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = off & 4 ? w[i + 2] : w[i];
+  for (int i = 0; i < 6; ++i) w[i] = off & 4 ? w[i + 2] : w[i];
 #pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = off & 2 ? w[i + 1] : w[i];
+  for (int i = 0; i < 5; ++i) w[i] = off & 2 ? w[i + 1] : w[i];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16 * (off & 1));
-    v = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i)
-      if (i < u.have) {
-        const uint32_t e = (uint32_t)__ldg(u.from + i) << (16 * (i % 2));
-        if (i < 2) w[0] |= e;
-        else if (i < 4) w[1] |= e;
-        else if (i < 6) w[2] |= e;
-        else w[3] |= e;
-      }
-    v = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < 4; ++i) {
+    const int left = have - 2 * i;
+    const uint32_t v = __funnelshift_r(w[i], w[i + 1], 16 * (off & 1));
+    w[i] = left >= 2 ? v : left == 1 ? v & 0xffffu : 0u;
   }
-  const uint32_t odd = u.have & 1 ? 0x0000ffffu : 0xffffffffu;  // of the word the row ends in
-  const int words = (u.have + 1) / 2;
-  v.x &= words == 1 ? odd : 0xffffffffu;
-  v.y &= words == 2 ? odd : words < 2 ? 0u : 0xffffffffu;
-  v.z &= words == 3 ? odd : words < 3 ? 0u : 0xffffffffu;
-  v.w &= words == 4 ? odd : words < 4 ? 0u : 0xffffffffu;
-  return v;
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Units 0 .. N - 1 of rows whose addresses are multiples of `grain` bytes (16, 8,
-// 4 or 2): asynchronous copies of that size, of rows of odd elements loads, four
-// units' together.  SHORT: see copy16_short.  WIDE: the grain is known to be 16
-// (the kernels are built with and without, for the checks of the others cost
-// the common case up to 15 %).
-template <int N, bool SHORT, bool WIDE, class F>
-__device__ __forceinline__ void copy_units(int grain, F unit) {
-  if (WIDE || grain == 16) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const Unit u = unit(i);
-      if (SHORT) copy16_short(u.to, u.from, 2 * u.have);
-      else copy16(u.to, u.from, 2 * u.have);
-    }
-  } else if (grain == 8) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const Unit u = unit(i);
-#pragma unroll
-      for (int o = 0; o < 8; o += 4) copy_small<8>(u.to + 2 * o, u.from + o, max(0, min(8, 2 * (u.have - o))));
-    }
-  } else if (grain == 4) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const Unit u = unit(i);
-#pragma unroll
-      for (int o = 0; o < 8; o += 2) copy_small<4>(u.to + 2 * o, u.from + o, max(0, min(4, 2 * (u.have - o))));
-    }
+// A row that is not aligned to 16 bytes comes as the two 16-byte words that each
+// of its units lies across, to `to` and `to + second`, and is shifted when it is
+// read back (take_raw).  Words that would leave the matrix are put together
+// element by element.
+__device__ __forceinline__ void copy_raw(const Unit& u, int second) {
+  if (u.have <= 0) return;
+  const int off = off_of(u.from);
+  if (u.before >= off && u.after >= 16 - off) {
+    copy16(u.to, u.from - off, 16);
+    copy16(u.to + second, u.from - off + 8, 16);
   } else {
-#pragma unroll
-    for (int i0 = 0; i0 < N; i0 += 4) {
-      uint4 v[4];
-#pragma unroll
-      for (int i = i0; i < i0 + 4; ++i)
-        if (i < N) v[i - i0] = load_unit(unit(i));
-#pragma unroll
-      for (int i = i0; i < i0 + 4; ++i)
-        if (i < N) *reinterpret_cast<uint4*>(unit(i).to) = v[i - i0];
-    }
+#pragma unroll 1
+    for (int i = 0; i < u.have; ++i)
+      *reinterpret_cast<uint16_t*>(u.to + (off + i >= 8 ? second - 16 : 0) + 2 * (off + i)) = __ldg(u.from + i);
   }
+}
+
+__device__ __forceinline__ uint4 take_raw(const unsigned char* at, int second, int off, int have) {
+  return shift_unit(*reinterpret_cast<const uint4*>(at), *reinterpret_cast<const uint4*>(at + second), off, have);
+}
+
+// The same at once, into registers.
+__device__ __forceinline__ uint4 load_unit(const Unit& u) {
+  const int off = off_of(u.from);
+  if (u.have > 0 && u.before >= off && u.after >= 16 - off) {
+    const uint4* at = reinterpret_cast<const uint4*>(u.from - off);
+    return shift_unit(__ldg(at), __ldg(at + 1), off, u.have);
+  }
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+  for (int i = 0; i < u.have; ++i) {
+    const uint32_t e = (uint32_t)__ldg(u.from + i) << (16 * (i % 2));
+    if (i < 2) w[0] |= e;
+    else if (i < 4) w[1] |= e;
+    else if (i < 6) w[2] |= e;
+    else w[3] |= e;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // ---- the first kernel's end: the cluster's sums to S
@@ -524,14 +501,15 @@ __device__ __forceinline__ void store_sums(const ApplyArgs& p, const float* sums
 // the ring needs no barrier.
 template <int RB>
 constexpr int kShrinkLowStages = RB == 4 ? 4 : 6;
-template <int RB>
-constexpr int kShrinkLowSmem = kLowWarps * kShrinkLowStages<RB> * (2 * RB + 1) * 512;
+template <int RB, bool WIDE>
+constexpr int kShrinkLowSmem = kLowWarps * kShrinkLowStages<RB> * (2 * RB + 1) * (WIDE ? 512 : 1024);
 
 template <bool BF16, int RB, bool WIDE>
 __global__ void __launch_bounds__(32 * kLowWarps)
 adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
   extern __shared__ __align__(16) unsigned char smem[];
-  constexpr int kStages = kShrinkLowStages<RB>, kStageBytes = (2 * RB + 1) * 512, R = RB * 16;
+  constexpr int kStages = kShrinkLowStages<RB>, kUnit = WIDE ? 512 : 1024, R = RB * 16;
+  constexpr int kStageBytes = (2 * RB + 1) * kUnit;
   grid_wait();
   // After the wait: what ran before this kernel is then complete for the next
   // one too, which reads the plan, B and base before its own wait.
@@ -558,24 +536,34 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
   unsigned char* ring = smem + warp * kStages * kStageBytes + lane * 16;
   const int steps = k1 > k0 ? max(0, ((k1 - k0 + kStep - 1) / kStep - warp + kLowWarps - 1) / kLowWarps) : 0;
   // Every copy of a step is made, those of rows that are not there with no
-  // bytes read and zeros written, so what is multiplied below needs no checks.
+  // bytes read and zeros written, so what is multiplied below needs no checks;
+  // rows that are not aligned to 16 bytes come raw and are cut to size there.
   int k = k_first, fetched = 0;
   unsigned char* to = ring;
   auto fetch = [&]() {
     if (fetched < steps) {
       const int have = max(0, min(8, k1 - k));
+      if (WIDE) {
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
-        if (b < blocks)
-          copy_units<2, false, WIDE>(p.grain_a[s], [&](int i) {
-            const int r = 16 * b + 8 * i + g;
-            const bool in = r < rank;
-            return Unit{to + (2 * b + i) * 512, A + (in ? r : 0) * a_row, in ? have : 0, r * a_row + k,
-                        (rank - 1 - r) * a_row + p.ad.cols - k};
-          });
-      copy_units<1, false, WIDE>(p.grain_x, [&](int) {
-        return Unit{to + 2 * RB * 512, x, have_x ? have : 0, row * p.ldx + k, (p.M - 1 - row) * p.ldx + p.ad.cols - k};
-      });
+        for (int b = 0; b < RB; ++b)
+          if (b < blocks) {
+#pragma unroll
+            for (int j = 2 * b; j < 2 * b + 2; ++j) {
+              const int r = 8 * j + g;
+              copy16(to + j * kUnit, A + (r < rank ? r : 0) * a_row, r < rank ? 2 * have : 0);
+            }
+          }
+        copy16(to + 2 * RB * kUnit, x, have_x ? 2 * have : 0);
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < 2 * blocks; ++j) {
+          const int r = 8 * j + g;
+          copy_raw(Unit{to + j * kUnit, A + r * a_row, r < rank ? have : 0, r * a_row + k,
+                        (rank - 1 - r) * a_row + p.ad.cols - k}, 512);
+        }
+        copy_raw(Unit{to + 2 * RB * kUnit, x, have_x ? have : 0, row * p.ldx + k,
+                      (p.M - 1 - row) * p.ldx + p.ad.cols - k}, 512);
+      }
       A += kLowWarps * kStep;
       x += kLowWarps * kStep;
       k += kLowWarps * kStep;
@@ -584,24 +572,35 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
     }
     copies_commit();
   };
+  int off[2 * RB + 1], read_k = k_first;
+  if (!WIDE) {
+#pragma unroll
+    for (int j = 0; j < 2 * RB; ++j) off[j] = off_of(A + (8 * j + g) * a_row);
+    off[2 * RB] = off_of(x);
+  }
   for (int i = 0; i < kStages - 1; ++i) fetch();
   float acc[RB][4] = {};
   const unsigned char* from = ring;
   for (int step = 0; step < steps; ++step) {
     copies_wait<kStages - 2>();
-    const uint4 v = *reinterpret_cast<const uint4*>(from + 2 * RB * 512);
+    const int have = max(0, min(8, k1 - read_k));
+    const unsigned char* x_at = from + 2 * RB * kUnit;
+    const uint4 v = WIDE ? *reinterpret_cast<const uint4*>(x_at) : take_raw(x_at, 512, off[2 * RB], have_x ? have : 0);
     uint4 w[2 * RB];
 #pragma unroll
     for (int b = 0; b < RB; ++b)
       if (b < blocks) {
-        w[2 * b] = *reinterpret_cast<const uint4*>(from + 2 * b * 512);
-        w[2 * b + 1] = *reinterpret_cast<const uint4*>(from + (2 * b + 1) * 512);
+#pragma unroll
+        for (int j = 2 * b; j < 2 * b + 2; ++j)
+          w[j] = WIDE ? *reinterpret_cast<const uint4*>(from + j * kUnit)
+                      : take_raw(from + j * kUnit, 512, off[j], 8 * j + g < rank ? have : 0);
       }
 #pragma unroll
     for (int half = 0; half < 2; ++half)
 #pragma unroll
       for (int b = 0; b < RB; ++b)
         if (b < blocks) mma_half<BF16>(half, acc[b], w[2 * b], w[2 * b + 1], v);
+    read_k += kLowWarps * kStep;
     from = from == ring + (kStages - 1) * kStageBytes ? ring : from + kStageBytes;
     fetch();
   }
@@ -609,7 +608,7 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
   // banks), added in order into [row][R], all over the rings.
   float* red = reinterpret_cast<float*>(smem);
   float* sums = red + kLowWarps * R * 9;
-  static_assert((kLowWarps * R * 9 + 8 * R) * 4 <= kShrinkLowSmem<RB>, "the sums lie over the rings");
+  static_assert((kLowWarps * R * 9 + 8 * R) * 4 <= kShrinkLowSmem<RB, WIDE>, "the sums lie over the rings");
   copies_wait<0>();
   __syncthreads();
 #pragma unroll
@@ -633,10 +632,16 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
 // stages.  Bound by the traffic from L2 (A again for every tile).  The tensor
 // cores cut off what an addition leaves below a sum's last bit, so the stages go
 // to four sums in turn, which are added in fp32, rounded.
+// Rows that are not aligned to 16 bytes (not WIDE) come raw, nine words for 64
+// elements, and each thread shifts what it copied into place when it is there.
+template <bool WIDE>
 struct ShrinkTallLayout {
-  static constexpr int kThreads = 128, kStages = 4, kCols = 64, kSlots = 128, kSums = 4;
+  static constexpr int kThreads = 128, kStages = WIDE ? 4 : 2, kCols = 64, kSlots = 128, kSums = 4;
   static constexpr int kStageBytes = (kSlots + kTall) * 128;   // rows of A, then rows of X
-  static constexpr int kBars = kStages * kStageBytes;          // a stage's products are done
+  static constexpr int kAhead = 3;                             // stages of copies on their way
+  static constexpr int kRawBytes = (kSlots + kTall) * 8 * 32;  // two words for each unit
+  static constexpr int kRaw = kStages * kStageBytes;
+  static constexpr int kBars = kRaw + (WIDE ? 0 : kAhead * kRawBytes);  // a stage's products are done
   static constexpr int kBytes = kBars + kStages * 8 + 8;       // tensor memory's address, give-up flag
   static constexpr int kColumns = kSums * kTall;
   static constexpr int kSumStride = kSlots + 4;
@@ -645,9 +650,9 @@ struct ShrinkTallLayout {
 constexpr uint64_t kTallWaitLimit = 2000000000ull;
 
 template <bool BF16, bool WIDE>
-__global__ void __launch_bounds__(ShrinkTallLayout::kThreads, 2)
+__global__ void __launch_bounds__(128, WIDE ? 2 : 1)
 adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
-  using L = ShrinkTallLayout;
+  using L = ShrinkTallLayout<WIDE>;
   static_assert(kTall * L::kSumStride * 4 <= L::kBars, "the sums lie over the stages");
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -685,9 +690,6 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
     const int place = row0 * 128 + (unit ^ (row0 & 7)) * 16;
     const uint16_t* src[kMine];
     unsigned there = 0;
-    int grain = 16;  // of all that the CTA copies
-    for (int s = 0; s < p.ad.slices; ++s) grain = min(grain, p.grain_a[s]);
-    grain = min(grain, p.grain_x);
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       const int row = row0 + 16 * i;
@@ -705,46 +707,43 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
         for (int st = 0; st < L::kStages; ++st)
           *reinterpret_cast<uint4*>(smem + st * L::kStageBytes + i * 2048 + place) = make_uint4(0u, 0u, 0u, 0u);
     }
-    auto unit_of = [&](int i, int step) {
-      const int k = k0 + step * L::kCols + 8 * unit;
-      const bool in = there >> i & 1;
-      // Within the row: its neighbours are not always ones of the same matrix.
-      return Unit{smem + step % L::kStages * L::kStageBytes + place + i * 2048, in ? src[i] + k : p.X,
-                  in ? max(0, min(8, k1 - k)) : 0, k, p.ad.cols - k};
-    };
-    // Rows of odd elements wait in registers from one step to the next.
-    uint4 late[WIDE ? 1 : kMine];
-    int late_step = steps;
     auto fetch = [&](int step) {
-      if (!WIDE && late_step < steps) {
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) *reinterpret_cast<uint4*>(unit_of(i, late_step).to) = late[WIDE ? 0 : i];
-        late_step = steps;
-      }
       if (step < steps) {
+        const int k = k0 + step * L::kCols + 8 * unit, have = max(0, min(8, k1 - k));
         if (WIDE) {
           unsigned char* to = smem + step % L::kStages * L::kStageBytes + place;
-          const int k = k0 + step * L::kCols + 8 * unit, bytes = max(0, min(16, 2 * (k1 - k)));
 #pragma unroll
           for (int i = 0; i < kMine; ++i)
-            if (there >> i & 1) copy16(to + i * 2048, src[i] + k, bytes);
-        } else if (grain > 2) {
-          copy_units<kMine, false, false>(grain, [&](int i) { return unit_of(i, step); });
+            if (there >> i & 1) copy16(to + i * 2048, src[i] + k, 2 * have);
         } else {
+          unsigned char* to = smem + L::kRaw + step % L::kAhead * L::kRawBytes + tid * 16;
 #pragma unroll
-          for (int i = 0; i < kMine; ++i) late[WIDE ? 0 : i] = load_unit(unit_of(i, step));
-          late_step = step;
+          for (int i = 0; i < kMine; ++i)  // within the row: its neighbours are not always the same matrix's
+            if (there >> i & 1) copy_raw(Unit{to + i * 4096, src[i] + k, have, k, p.ad.cols - k}, 2048);
         }
       }
       copies_commit();
     };
-    for (int i = 0; i < L::kStages - 1; ++i) fetch(i);
+    for (int i = 0; i < L::kAhead; ++i) fetch(i);
     const uint32_t idesc = tc::idesc_f16(kTall, BF16 ? 1 : 0);
+    auto wait_for = [&](int step) {
+      ok = tc::mbar_wait_or_abort(bars + 8 * (step % L::kStages), (step / L::kStages) & 1, kTallWaitLimit, slot + 1) && ok;
+    };
     for (int step = 0; step < steps; ++step) {
-      copies_wait<L::kStages - 2>();
+      copies_wait<L::kAhead - 1>();
+      const int st = step % L::kStages;
+      if (!WIDE) {
+        if (step >= L::kStages) wait_for(step - L::kStages);  // the stage is free
+        const int k = k0 + step * L::kCols + 8 * unit, have = max(0, min(8, k1 - k));
+        const unsigned char* raw = smem + L::kRaw + step % L::kAhead * L::kRawBytes + tid * 16;
+        unsigned char* to = smem + st * L::kStageBytes + place;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+          if (there >> i & 1)
+            *reinterpret_cast<uint4*>(to + i * 2048) = take_raw(raw + i * 4096, 2048, off_of(src[i] + k), have);
+      }
       tc::fence_proxy_async();
       __syncthreads();
-      const int st = step % L::kStages;
       if (warp == 0) {
         const uint64_t w = tc::smem_desc_sw128(tc::smem_u32(smem + st * L::kStageBytes));
         const uint64_t x = w + L::kSlots * 128 / 16;
@@ -754,14 +753,11 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
         tc::mma_commit_warp(bars + 8 * st);
       }
       // The stage before this one is read: its place takes the step after next.
-      if (step > 0)
-        ok = tc::mbar_wait_or_abort(bars + 8 * ((step - 1) % L::kStages), ((step - 1) / L::kStages) & 1, kTallWaitLimit,
-                                    slot + 1) && ok;
-      fetch(step + L::kStages - 1);
+      if (WIDE && step > 0) wait_for(step - 1);
+      fetch(step + L::kAhead);
     }
-    if (steps > 0)
-      ok = tc::mbar_wait_or_abort(bars + 8 * ((steps - 1) % L::kStages), ((steps - 1) / L::kStages) & 1, kTallWaitLimit,
-                                  slot + 1) && ok;
+    if (!WIDE && steps > 1) wait_for(steps - 2);
+    if (steps > 0) wait_for(steps - 1);
     tc::fence_after_sync();
     copies_wait<0>();
     __syncthreads();  // the stages are read by all: the sums go over them
@@ -842,16 +838,16 @@ __device__ __forceinline__ bool expand_tile(const ApplyArgs& p, int chunks, int 
 // the ring is 32 outputs and a block of up to 64 ranks (32 KC); the last of an
 // output's items brings base.
 constexpr int kLowStages = 3;
-template <int KC>
-constexpr int kLowItemBytes = 2048 * KC + 1024;
-template <int KC>
-constexpr int kExpandLowSmem = kLowWarps * kLowStages * kLowItemBytes<KC>;
+template <int KC, bool WIDE>
+constexpr int kLowItemBytes = 2048 * KC * (WIDE ? 1 : 2) + 1024;
+template <int KC, bool WIDE>
+constexpr int kExpandLowSmem = kLowWarps * kLowStages * kLowItemBytes<KC, WIDE>;
 
 template <bool BF16, int KC, bool MANY, bool WIDE>
 __global__ void __launch_bounds__(32 * kLowWarps)
 adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int in_place) {
   extern __shared__ __align__(16) unsigned char smem[];
-  constexpr int P = kParts<BF16>, kItemBytes = kLowItemBytes<KC>, kRound = 32 * kLowWarps;
+  constexpr int P = kParts<BF16>, kItemBytes = kLowItemBytes<KC, WIDE>, kRound = 32 * kLowWarps;
   grid_launch_dependents();
   ExpandTile x;
   if (!expand_tile(p, chunks, in_place, x)) {
@@ -863,6 +859,7 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
   const uint16_t* B = static_cast<const uint16_t*>(p.ad.B[x.s]) + max(x.a, 0) * p.ad.b_adapter[x.s];
   const int64_t b_row = p.ad.b_row[x.s];
   const bool vec_y = p.grain_y[x.s] == 16;
+  const bool eights = p.grain_b[x.s] >= 8;  // rows of B that 8-byte copies can fetch
   const float* from[2];
   float* to[2];
 #pragma unroll
@@ -894,11 +891,21 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int n = fetch_n + 4 * g + j;
-        copy_units<KC, true, WIDE>(p.grain_b[x.s], [&](int c) {
-          return Unit{into + (4 * c + j) * 512, b + kStep * c, whole || n < x.c1 ? have[c] : 0,
-                      n * b_row + fetch_k + kStep * c + 8 * q,
-                      (p.ad.rows[x.s] - 1 - n) * b_row + x.rank - fetch_k - kStep * c - 8 * q};
-        });
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          const int wanted = whole || n < x.c1 ? have[c] : 0;
+          unsigned char* to = into + (4 * c + j) * 512;
+          const uint16_t* from = b + kStep * c;
+          if (WIDE) {
+            copy16_short(to, from, 2 * wanted);
+          } else if (eights) {
+            copy_small<8>(to, from, max(0, min(8, 2 * wanted)));
+            copy_small<8>(to + 8, from + 4, max(0, 2 * wanted - 8));
+          } else {
+            const int r = fetch_k + kStep * c + 8 * q;
+            copy_raw(Unit{to, from, wanted, n * b_row + r, (p.ad.rows[x.s] - 1 - n) * b_row + x.rank - r}, 2048 * KC);
+          }
+        }
         b += b_row;
       }
       b_next += 64;
@@ -959,7 +966,12 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
       if (k + kStep * c >= x.rank) break;
       uint4 w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint4*>(item_at + (4 * c + j) * 512);
+      for (int j = 0; j < 4; ++j) {
+        const unsigned char* at = item_at + (4 * c + j) * 512;
+        const int n = n0 + 4 * g + j, r = k + kStep * c + 8 * q;
+        w[j] = WIDE || eights ? *reinterpret_cast<const uint4*>(at)
+                              : take_raw(at, 2048 * KC, off_of(B + n * b_row + r), n < x.c1 ? max(0, min(8, x.rank - r)) : 0);
+      }
 #pragma unroll
       for (int half = 0; half < 2; ++half)
 #pragma unroll
@@ -1097,12 +1109,35 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const int have = max(0, min(8, rank - 64 * b - 8 * unit));
-        copy_units<16, true, WIDE>(p.grain_b[s], [&](int u) {
+        auto unit_of = [&](int u) {
           const int j = u / 2, h = u % 2, at = n + 32 * j + h;
           return Unit{to + (h * NB + b) * 128 * 128 + j * 16 * 128, src + 64 * b + (32 * j + h) * b_row,
                       at < rows ? have : 0, at * b_row + 64 * b + 8 * unit,
                       (rows - 1 - at) * b_row + rank - 64 * b - 8 * unit};
-        });
+        };
+        if (WIDE) {
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            const Unit x = unit_of(u);
+            copy16_short(x.to, x.from, 2 * x.have);
+          }
+        } else if (p.grain_b[s] >= 8) {
+#pragma unroll 2
+          for (int u = 0; u < 16; ++u) {
+            const Unit x = unit_of(u);
+            copy_small<8>(x.to, x.from, max(0, min(8, 2 * x.have)));
+            copy_small<8>(x.to + 8, x.from + 4, max(0, 2 * x.have - 8));
+          }
+        } else {
+#pragma unroll 1
+          for (int u0 = 0; u0 < 16; u0 += 4) {
+            uint4 v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[u] = load_unit(unit_of(u0 + u));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(unit_of(u0 + u).to) = v[u];
+          }
+        }
       }
       copies_commit();
     };
@@ -1287,9 +1322,9 @@ ShrinkShape shrink_shape(const seedlm_adapters& ad, int M, const DeviceInfo& dev
     clusters *= sh.groups * ad.slices;
     round = kLowWarps * 4;
   } else {
-    sh.groups = (ad.slices * sh.slots + ShrinkTallLayout::kSlots - 1) / ShrinkTallLayout::kSlots;
+    sh.groups = (ad.slices * sh.slots + ShrinkTallLayout<true>::kSlots - 1) / ShrinkTallLayout<true>::kSlots;
     clusters *= sh.groups;
-    round = ShrinkTallLayout::kStages * ShrinkTallLayout::kCols / kStep;
+    round = ShrinkTallLayout<true>::kStages * ShrinkTallLayout<true>::kCols / kStep;
   }
   // Low: enough CTAs for three on each SM.  Tall: no more than the two that fit
   // one (a second round of CTAs costs more than their shorter parts save; 4096
@@ -1321,19 +1356,19 @@ int launch_products_kernel(Kernel kernel, int64_t grid, int threads, int smem, i
 template <bool BF16, bool WIDE, int RB>
 int launch_shrink_low(const ApplyArgs& p, int64_t tiles, int splits, cudaStream_t stream, const DeviceInfo& dev) {
   return launch_products_kernel(adapters_shrink_low_kernel<BF16, RB, WIDE>, tiles * p.ad.slices * p.groups * splits,
-                                32 * kLowWarps, kShrinkLowSmem<RB>, splits, stream, dev, p);
+                                32 * kLowWarps, kShrinkLowSmem<RB, WIDE>, splits, stream, dev, p);
 }
 
 template <bool BF16, bool WIDE>
 int launch_shrink_tall(const ApplyArgs& p, int64_t tiles, int splits, cudaStream_t stream, const DeviceInfo& dev) {
-  using L = ShrinkTallLayout;
+  using L = ShrinkTallLayout<WIDE>;
   return launch_products_kernel(adapters_shrink_tall_kernel<BF16, WIDE>, tiles * p.groups * splits, L::kThreads, L::kBytes,
                                 splits, stream, dev, p);
 }
 
 template <bool BF16, bool WIDE, int KC, bool MANY>
 int launch_expand_low(const ApplyArgs& p, int64_t grid, int chunks, cudaStream_t stream, const DeviceInfo& dev) {
-  return launch_products_kernel(adapters_expand_low_kernel<BF16, KC, MANY, WIDE>, grid, 32 * kLowWarps, kExpandLowSmem<KC>, 1,
+  return launch_products_kernel(adapters_expand_low_kernel<BF16, KC, MANY, WIDE>, grid, 32 * kLowWarps, kExpandLowSmem<KC, WIDE>, 1,
                                 stream, dev, p, chunks, (int)(p.base == p.Y));
 }
 
