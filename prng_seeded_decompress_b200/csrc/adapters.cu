@@ -26,20 +26,17 @@ __device__ unsigned int g_wait_error;
 // ---------------------------------------------------------------- the plan
 //
 // Layout in int32 words: [0, M) order, [M, M + n + 1) offsets, then from the
-// next multiple of 4: {M, n, tiles of rows with an adapter, all tiles} and
-// one int4 {adapter or -1, first, count, 0} for each tile of up to
-// adapter_tile_rows(M) rows of one adapter, in sorted order.
+// next multiple of 4, for tiles of up to 8 rows and for tiles of up to 64, a head
+// {M, n, tiles of rows with an adapter, all tiles}; then for each of the two an
+// int4 {adapter or -1, first, count, 0} for every tile, in sorted order.  Each
+// projection takes the one that suits it.
+
+constexpr int kLowRows = 8, kTall = 64;
 
 __host__ __device__ inline int64_t plan_tail(int64_t M, int64_t n) { return (M + n + 1 + 3) / 4 * 4; }
 
-// Rows of a tile: short tiles for batches where most requests have their own
-// adapter, tall ones where an adapter's rows share its matrices.
-__host__ __device__ inline int adapter_tile_rows(int M) { return M <= 256 ? 8 : 64; }
-
 // Every bin of c rows takes at most c / T + 1 tiles.
-inline int64_t max_tiles(int64_t M, int64_t n) {
-  return M / adapter_tile_rows((int)M) + (M < n + 1 ? M : n + 1);
-}
+__host__ __device__ inline int64_t max_tiles(int64_t M, int64_t n, int T) { return M / T + (M < n + 1 ? M : n + 1); }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -78,8 +75,7 @@ __device__ __forceinline__ int load_of_cta(const int* mine, uint32_t cta) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1)
-adapters_plan_kernel(int M, int n, int T, const int32_t* __restrict__ ids, int32_t* __restrict__ plan,
-                     int64_t tail_words) {
+adapters_plan_kernel(int M, int n, const int32_t* __restrict__ ids, int32_t* __restrict__ plan) {
   extern __shared__ int32_t sm[];
   const int bins = n + 1, nwarps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cta = (int)cluster_rank(), ctas = (int)cluster_size();
@@ -87,9 +83,9 @@ adapters_plan_kernel(int M, int n, int T, const int32_t* __restrict__ ids, int32
   int32_t* total = hist + (size_t)nwarps * bins;  // [bins] rows of each bin in this CTA
   int32_t* base = total + bins;                   // [bins] place of this CTA's first row of each bin
   int32_t* start = base + bins;                   // [bins + 1] of all CTAs
-  int32_t* tstart = start + bins + 1;             // [bins + 1] tiles before each bin
-  int32_t* warp_rows = tstart + bins + 1;         // [nwarps]
-  int32_t* warp_tiles = warp_rows + nwarps;       // [nwarps]
+  int32_t* low_start = start + bins + 1;          // [bins + 1] low tiles before each bin
+  int32_t* tall_start = low_start + bins + 1;     // [bins + 1] tall ones
+  int32_t* warp_sums = tall_start + bins + 1;     // [3][32]
   grid_launch_dependents();
   for (int i = threadIdx.x; i < nwarps * bins; i += blockDim.x) hist[i] = 0;
   grid_wait();
@@ -137,7 +133,7 @@ adapters_plan_kernel(int M, int n, int T, const int32_t* __restrict__ ids, int32
   // Every CTA scans all bins, each thread taking `per` consecutive ones.
   const int per = (bins + blockDim.x - 1) / blockDim.x;
   const int b0 = min(bins, (int)threadIdx.x * per), b1 = min(bins, b0 + per);
-  int rows = 0, tiles = 0;
+  int mine3[3] = {0, 0, 0};  // rows, low tiles, tall tiles
   for (int b = b0; b < b1; ++b) {
     int before = 0, all = 0;
     if (ctas == 1) {
@@ -150,39 +146,45 @@ adapters_plan_kernel(int M, int n, int T, const int32_t* __restrict__ ids, int32
         if (c < cta) before += v;
       }
     }
-    start[b] = rows;  // within this thread's bins
-    tstart[b] = tiles;
+    start[b] = mine3[0];  // within this thread's bins
+    low_start[b] = mine3[1];
+    tall_start[b] = mine3[2];
     base[b] = before;
-    rows += all;
-    tiles += (all + T - 1) / T;
+    mine3[0] += all;
+    mine3[1] += (all + kLowRows - 1) / kLowRows;
+    mine3[2] += (all + kTall - 1) / kTall;
   }
-  int2 incl = make_int2(rows, tiles);
+  int before3[3];
 #pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const int x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
-    if (lane >= o) incl = make_int2(incl.x + x, incl.y + y);
-  }
-  if (lane == 31) {
-    warp_rows[warp] = incl.x;
-    warp_tiles[warp] = incl.y;
+  for (int j = 0; j < 3; ++j) {
+    int incl = mine3[j];
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sums[32 * j + warp] = incl;
+    before3[j] = incl - mine3[j];
   }
   __syncthreads();
-  // Sums of the warps before this one, a lane each.
-  int2 before = make_int2(lane < warp ? warp_rows[lane] : 0, lane < warp ? warp_tiles[lane] : 0);
 #pragma unroll
-  for (int o = 16; o > 0; o /= 2)
-    before = make_int2(before.x + __shfl_xor_sync(0xffffffffu, before.x, o),
-                       before.y + __shfl_xor_sync(0xffffffffu, before.y, o));
-  before = make_int2(before.x + incl.x - rows, before.y + incl.y - tiles);
+  for (int j = 0; j < 3; ++j) {  // of the warps before this one, a lane each
+    int v = lane < warp ? warp_sums[32 * j + lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    before3[j] += v;
+  }
   for (int b = b0; b < b1; ++b) {
-    start[b] += before.x;
-    tstart[b] += before.y;
+    start[b] += before3[0];
+    low_start[b] += before3[1];
+    tall_start[b] += before3[2];
     base[b] += start[b];
     if (cta == 0) plan[M + b] = start[b];
   }
   if (b1 == bins && b0 < bins) {  // the thread of the last bin
-    start[bins] = before.x + rows;
-    tstart[bins] = before.y + tiles;
+    start[bins] = before3[0] + mine3[0];
+    low_start[bins] = before3[1] + mine3[1];
+    tall_start[bins] = before3[2] + mine3[2];
   }
   __syncthreads();
   for (int r = r0; r < r1; r += 32 * kPlanSteps) {
@@ -202,20 +204,24 @@ adapters_plan_kernel(int M, int n, int T, const int32_t* __restrict__ ids, int32
       __syncwarp();
     }
   }
-  int32_t* tail = plan + plan_tail(M, n);
-  const int all = tstart[bins];
-  if (cta == 0 && threadIdx.x == 0) *reinterpret_cast<int4*>(tail) = make_int4(M, n, tstart[n], all);
-  for (int t = cta * blockDim.x + threadIdx.x; t < all; t += ctas * blockDim.x) {
-    int lo = 0, hi = bins - 1;  // the last bin that starts at or before tile t
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (tstart[mid] <= t) lo = mid;
-      else hi = mid - 1;
+  int4* tail = reinterpret_cast<int4*>(plan + plan_tail(M, n));
+  auto list = [&](int T, const int32_t* first, int4* head, int4* to) {
+    const int all = first[bins];
+    if (cta == 0 && threadIdx.x == 0) *head = make_int4(M, n, first[n], all);
+    for (int t = cta * blockDim.x + threadIdx.x; t < all; t += ctas * blockDim.x) {
+      int lo = 0, hi = bins - 1;  // the last bin that starts at or before tile t
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (first[mid] <= t) lo = mid;
+        else hi = mid - 1;
+      }
+      const int at = start[lo] + (t - first[lo]) * T;
+      if (SEEDLM_IN_BOUNDS(g_check_flag, t, max_tiles(M, n, T)))
+        to[t] = make_int4(lo < n ? lo : -1, at, min(T, start[lo + 1] - at), 0);
     }
-    const int at = start[lo] + (t - tstart[lo]) * T;
-    if (SEEDLM_IN_BOUNDS(g_check_flag, 4 + 4 * (int64_t)t + 3, tail_words))
-      reinterpret_cast<int4*>(tail)[1 + t] = make_int4(lo < n ? lo : -1, at, min(T, start[lo + 1] - at), 0);
-  }
+  };
+  list(kLowRows, low_start, tail, tail + 2);
+  list(kTall, tall_start, tail + 1, tail + 2 + max_tiles(M, n, kLowRows));
   if (ctas > 1) cluster_sync();  // no CTA leaves while another reads its totals
 }
 
@@ -234,7 +240,6 @@ adapters_plan_kernel(int M, int n, int T, const int32_t* __restrict__ ids, int32
 
 constexpr int kLowWarps = 4;   // of the kernels for low tiles
 constexpr int kStep = 32;      // contraction elements of one 16-byte load per lane
-constexpr int kTall = 64;      // rows of a tall tile
 constexpr int kMaxSplits = 8;  // CTAs of a cluster that share the first contraction
 
 // The parts of a sum that 16-bit operands hold.  bf16 has fp32's range: three
@@ -249,6 +254,7 @@ constexpr int kParts = BF16 ? 3 : 2;
 struct ApplyArgs {
   seedlm_adapters ad;
   const int32_t* plan;
+  const int4 *head, *tiles;  // the plan's, of the tiles that are taken
   int M;
   const uint16_t* X;
   int64_t ldx;
@@ -269,12 +275,10 @@ struct ApplyArgs {
   int grain_x, grain_a[SEEDLM_MAX_SLICES], grain_b[SEEDLM_MAX_SLICES], grain_y[SEEDLM_MAX_SLICES];
 };
 
-__device__ __forceinline__ const int32_t* plan_tail_of(const ApplyArgs& p) { return p.plan + plan_tail(p.M, p.ad.n); }
-
 // The plan's head, {M, n, tiles with an adapter, tiles}, with no tiles at all if
 // it does not belong to this call.
 __device__ __forceinline__ int4 plan_head(const ApplyArgs& p) {
-  int4 head = *reinterpret_cast<const int4*>(plan_tail_of(p));
+  int4 head = *p.head;
   if (head.x != p.M || head.y != p.ad.n) {
     if (threadIdx.x == 0) atomicOr(&g_plan_mismatch, 1u);
     head.z = head.w = 0;
@@ -285,7 +289,7 @@ __device__ __forceinline__ int4 plan_head(const ApplyArgs& p) {
 // Tile t {adapter or -1, first, rows, 0}; t below the plan's room, whether the
 // plan has so many or not.
 __device__ __forceinline__ int4 plan_tile(const ApplyArgs& p, int64_t t) {
-  return reinterpret_cast<const int4*>(plan_tail_of(p))[1 + t];
+  return p.tiles[t];
 }
 
 __device__ __forceinline__ int rank_of(const seedlm_adapters& ad, int a) {
@@ -1285,7 +1289,9 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
 
 }  // namespace
 
-int64_t adapters_plan_words(int M, int n) { return plan_tail(M, n) + 4 + 4 * max_tiles(M, n); }
+int64_t adapters_plan_words(int M, int n) {
+  return plan_tail(M, n) + 4 * (2 + max_tiles(M, n, kLowRows) + max_tiles(M, n, kTall));
+}
 
 int launch_adapters_plan(int M, int n, const int32_t* ids, int32_t* plan, cudaStream_t stream, const DeviceInfo& dev) {
   int rc = allow_max_smem((const void*)adapters_plan_kernel, dev);
@@ -1296,9 +1302,8 @@ int launch_adapters_plan(int M, int n, const int32_t* ids, int32_t* plan, cudaSt
   const int most = M > n + 1 ? M : n + 1;
   const int threads = most >= kPlanThreads ? kPlanThreads : (most + 31) / 32 * 32;
   const int nwarps = threads / 32, bins = n + 1;
-  const size_t smem = ((size_t)nwarps * bins + 4 * bins + 2 + 2 * nwarps) * sizeof(int32_t);
-  return launch_pdl_cluster(adapters_plan_kernel, ctas, threads, smem, ctas, stream, M, n, adapter_tile_rows(M), ids,
-                            plan, adapters_plan_words(M, n) - plan_tail(M, n));
+  const size_t smem = ((size_t)nwarps * bins + 5 * bins + 3 + 3 * 32) * sizeof(int32_t);
+  return launch_pdl_cluster(adapters_plan_kernel, ctas, threads, smem, ctas, stream, M, n, ids, plan);
 }
 
 namespace {
@@ -1308,15 +1313,33 @@ namespace {
 // columns in as many parts (CTAs of a cluster) as fill the GPU when there
 // are few tiles, none so short that its rings are not filled once.
 struct ShrinkShape {
+  bool low;
+  int64_t tiles;  // at most
   int slots, blocks, groups, splits, split_cols;
 };
+
+// Whether a projection takes tiles of 8 rows or of 64.  In units of 57344 outputs
+// and inputs, a low tile was measured at 1.65 us whatever its rows and ranks, a
+// tall one at 3.75 us and 0.03 us a row, and its two kernels at 13 us more for
+// their longer start (8192 x 8192 and 28672+28672 x 8192, ranks 16 and 64, 1 to
+// 64 adapters, 16 to 2048 rows; e.g. 8 adapters of rank 64 on the larger: 41 us
+// low, 51 tall at 128 rows, 71 and 57 at 256).  The rows are taken to be spread
+// evenly over the adapters.
+bool takes_low_tiles(const seedlm_adapters& ad, int M) {
+  double size = (double)ad.slices * ad.cols;
+  for (int s = 0; s < ad.slices; ++s) size += ad.rows[s];
+  const int used = std::min(M, ad.n), each = (M + used - 1) / used;
+  const double low = (double)used * ((each + kLowRows - 1) / kLowRows), tall = (double)used * ((each + kTall - 1) / kTall);
+  return size / 57344 * (1.65 * low - 3.75 * tall - 0.03 * M) <= 13;
+}
 
 ShrinkShape shrink_shape(const seedlm_adapters& ad, int M, const DeviceInfo& dev) {
   ShrinkShape sh{};
   sh.slots = ad.rank <= 32 ? 32 : (ad.rank + 63) / 64 * 64;
-  int64_t clusters = max_tiles(M, ad.n), round;
-  const bool low = adapter_tile_rows(M) == 8;
-  if (low) {
+  sh.low = takes_low_tiles(ad, M);
+  sh.tiles = max_tiles(M, ad.n, sh.low ? kLowRows : kTall);
+  int64_t clusters = sh.tiles, round;
+  if (sh.low) {
     sh.blocks = sh.slots == 32 ? 2 : 4;
     sh.groups = sh.slots / (16 * sh.blocks);
     clusters *= sh.groups * ad.slices;
@@ -1332,7 +1355,7 @@ ShrinkShape shrink_shape(const seedlm_adapters& ad, int M, const DeviceInfo& dev
   const int64_t steps = (ad.cols + kStep - 1) / kStep;
   sh.splits = 1;
   while (sh.splits < kMaxSplits && steps >= 2 * sh.splits * round &&
-         (low ? sh.splits * clusters < 3 * dev.num_sms : sh.splits * clusters <= dev.num_sms))
+         (sh.low ? sh.splits * clusters < 3 * dev.num_sms : sh.splits * clusters <= dev.num_sms))
     sh.splits *= 2;
   // Parts begin at whole stages of either form.
   sh.split_cols = (int)(((steps + sh.splits - 1) / sh.splits + 1) / 2 * 2 * kStep);
@@ -1382,7 +1405,7 @@ int launch_expand_tall(const ApplyArgs& p, int64_t items, int chunks, cudaStream
 
 template <bool BF16, bool WIDE>
 int launch_products(ApplyArgs& p, const ShrinkShape& sh, int64_t tiles, cudaStream_t stream, const DeviceInfo& dev) {
-  const bool low = adapter_tile_rows(p.M) == 8;
+  const bool low = sh.low;
   int rc;
   if (low)
     rc = sh.blocks == 4 ? launch_shrink_low<BF16, WIDE, 4>(p, tiles, sh.splits, stream, dev)
@@ -1463,7 +1486,9 @@ int launch_adapters_apply(const seedlm_adapters& ad, const int32_t* plan, int M,
     at += ad.rows[s];
   }
   p.grain_x = grain_of(X, 2 * ldx, 0);
-  const int64_t tiles = max_tiles(M, ad.n);
+  const int64_t tiles = sh.tiles;
+  p.head = reinterpret_cast<const int4*>(plan + plan_tail(M, ad.n)) + (sh.low ? 0 : 1);
+  p.tiles = reinterpret_cast<const int4*>(plan + plan_tail(M, ad.n)) + 2 + (sh.low ? 0 : max_tiles(M, ad.n, kLowRows));
   if (tiles * ad.slices * sh.groups * sh.splits > INT32_MAX) return SEEDLM_EUNSUPPORTED;
   bool wide = p.grain_x == 16;
   for (int s = 0; s < ad.slices; ++s) wide = wide && p.grain_a[s] == 16 && p.grain_b[s] == 16;
