@@ -244,15 +244,23 @@ def apply(sl, d, Y, base=None, workspace=None, plan=None, stream=None):
     return Y
 
 
-#: M, cols, rows of the slices, adapters, rank: one token to many, both tile
-#: heights, sides that divide nothing, one of everything, every slice count.
-SHAPES = [
+#: M, cols, rows of the slices, adapters, rank: one token to many, sides that
+#: divide nothing, one of everything, every slice count.
+LOW = [
     (1, 64, [32], 1, 8), (1, 8192, [1024], 3, 16), (2, 1, [1], 2, 1), (3, 7, [5], 2, 3), (5, 4099, [1021], 4, 12),
     (8, 256, [128], 1, 16), (9, 256, [128], 1, 64), (64, 512, [96, 40], 64, 20), (37, 1024, [256, 64, 64], 20, 16),
     (100, 300, [33, 1, 70, 31], 6, 37), (255, 96, [64], 300, 8), (256, 130, [130], 5, 130), (257, 130, [130], 5, 130),
     (300, 1000, [500], 1, 256), (333, 513, [127], 7, 12), (700, 64, [1000, 24], 3, 16), (1025, 264, [72], 1024, 4),
     (17, 20000, [16], 2, 256), (600, 9001, [64], 2, 8), (64, 0, [40], 3, 8),
 ]
+#: The same for batches that take tiles of 64 rows.
+TALL = [
+    (2000, 2000, [2000], 3, 16), (2100, 4099, [1021], 7, 12), (1500, 2048, [1024, 512, 520], 2, 64),
+    (3000, 1000, [2001, 33], 5, 37), (1200, 3001, [4000], 1, 130), (1300, 2500, [3000], 2, 256),
+    (2600, 64, [6000], 9, 4), (2500, 9000, [64], 2, 8), (4096, 1024, [2048], 40, 20), (3000, 0, [9000], 2, 8),
+    (2049, 1, [7001], 1, 1), (1800, 5000, [258], 2, 97),
+]
+SHAPES = LOW + TALL
 
 
 @pytest.mark.gpu
@@ -291,17 +299,17 @@ def test_normal_numbers_within_the_bound(gpu, M, cols, rows, n, rank, dtype):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M", [1, 40, 300])
-def test_sums_between_the_products_keep_24_bits_whatever_their_size(gpu, M):
-    # x A^T of very different sizes in one row (2^-20 to 2^20 of each other):
-    # the outputs that take only the small one must see it whole.
+@pytest.mark.parametrize("M,outs", [(1, 16), (40, 16), (2048, 6000)])
+def test_sums_between_the_products_keep_24_bits_whatever_their_size(gpu, M, outs):
+    # x A^T of very different sizes in one row (2^-15 to 1 of each other): the
+    # outputs that take only the small one must see it whole.
     n, rank, cols = 1, 16, 32
     for dtype in ("bf16", "f16"):
         A = torch.zeros(n, rank, cols)
-        B = torch.zeros(n, rank, rank)
+        B = torch.zeros(n, outs, rank)
         for r in range(rank):
             A[0, r, 2 * r], A[0, r, 2 * r + 1] = 1.0, 2.0 ** -8
-            B[0, r, r] = 1.0
+            B[0, r::rank, r] = 1.0
         X = torch.zeros(M, cols)
         for r in range(rank):
             X[:, 2 * r] = 2.0 ** (r - 8) * 1.5
@@ -309,24 +317,24 @@ def test_sums_between_the_products_keep_24_bits_whatever_their_size(gpu, M):
         dt = DT[dtype]
         ad = gpu.Adapters(A.to(dt).cuda(), B.to(dt).cuda())
         plan = gpu.adapter_plan(torch.zeros(M, dtype=torch.int32, device="cuda"), n)
-        Y = torch.zeros(M, rank, device="cuda")
+        Y = torch.zeros(M, outs, device="cuda")
         gpu.adapter_apply(ad, plan, X.to(dt).cuda(), Y)
-        want = torch.tensor([2.0 ** (r - 8) * (1.5 + 1.25 * 2.0 ** -8) for r in range(rank)]).expand(M, rank)
+        want = torch.tensor([2.0 ** (r % rank - 8) * (1.5 + 1.25 * 2.0 ** -8) for r in range(outs)]).expand(M, outs)
         assert torch.equal(Y.cpu(), want)
 
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("M", [6, 290])
-def test_infinities_and_nan_stay_in_their_rows(gpu, M, dtype):
-    d = make(M, 200, [90], 2, 9, dtype, "whole", 5, none=0.0, ranks="full")
+@pytest.mark.parametrize("M,outs", [(6, 90), (290, 90), (2048, 6000)])
+def test_infinities_and_nan_stay_in_their_rows(gpu, M, outs, dtype):
+    d = make(M, 200, [outs], 2, 9, dtype, "whole", 5, none=0.0, ranks="full")
     d["ids"].zero_()
-    clean = apply(gpu, d, torch.empty(M, 90, device="cuda"), base=d["base"])
+    clean = apply(gpu, d, torch.empty(M, outs, device="cuda"), base=d["base"])
     d["X"][1, 3], d["X"][4, 0] = float("nan"), float("inf")
     d["A"][0][0, :, 0] = 1.0  # the infinity reaches every sum with one sign ...
     d["B"][0][0] = 2.0        # ... and every output
     ref, _ = reference(d)
-    Y = apply(gpu, d, torch.empty(M, 90, device="cuda"), base=d["base"])
+    Y = apply(gpu, d, torch.empty(M, outs, device="cuda"), base=d["base"])
     assert bool(Y[1].isnan().all())
     assert bool((Y[4] == float("inf")).all())
     keep = [m for m in range(M) if m not in (1, 4)]
@@ -335,9 +343,9 @@ def test_infinities_and_nan_stay_in_their_rows(gpu, M, dtype):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M", [4, 300])
-def test_rows_without_an_adapter_are_left_alone(gpu, M):
-    d = make(M, 128, [64, 10], 3, 8, "bf16", "whole", 9, none=0.5)
+@pytest.mark.parametrize("M,cols,rows", [(4, 128, [64, 10]), (300, 128, [64, 10]), (4000, 2000, [1900, 102])])
+def test_rows_without_an_adapter_are_left_alone(gpu, M, cols, rows):
+    d = make(M, cols, rows, 3, 8, "bf16", "whole", 9, none=0.5)
     d["ids"][0] = -1
     off = (d["ids"] < 0).nonzero().flatten()
     d["X"][off] = float("nan")
@@ -424,16 +432,16 @@ def test_a_workspace_that_is_too_small_or_misaligned_is_refused(gpu):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M", [12, 400])
-def test_captured_graphs_that_share_a_workspace_and_follow_their_inputs(gpu, M):
+@pytest.mark.parametrize("M,cols,rows", [(12, 512, [200, 56]), (400, 512, [200, 56]), (2048, 1024, [1500, 548])])
+def test_captured_graphs_that_share_a_workspace_and_follow_their_inputs(gpu, M, cols, rows):
     n = 6
-    d = make(M, 512, [200, 56], n, 16, "bf16", "whole", 21)
-    e = make(M, 512, [200, 56], n, 16, "bf16", "whole", 22)
+    d = make(M, cols, rows, n, 16, "bf16", "whole", 21)
+    e = make(M, cols, rows, n, 16, "bf16", "whole", 22)
     ads = [gpu.Adapters(v["A"], v["B"], ranks=v["ranks"], scales=v["scales"]) for v in (d, e)]
     ws = gpu.adapter_workspace(ads[0], M)
     ws.fill_(255)  # any content
     plans = [gpu.AdapterPlan(M, n) for _ in ads]
-    Ys = [torch.empty(M, 256, device="cuda") for _ in ads]
+    Ys = [torch.empty(M, sum(rows), device="cuda") for _ in ads]
     graphs = []
     gpu.adapter_plan(d["ids"], n, plan=plans[0])
     gpu.adapter_apply(ads[0], plans[0], d["X"], Ys[0], base=d["base"], workspace=ws)
@@ -459,13 +467,14 @@ def test_captured_graphs_that_share_a_workspace_and_follow_their_inputs(gpu, M):
 
 
 @pytest.mark.gpu
-def test_streams_of_their_own(gpu):
-    ds = [make(70, 1024, [300], 5, 16, "f16", "whole", 31 + i) for i in range(3)]
+@pytest.mark.parametrize("M,cols,outs", [(70, 1024, 300), (2048, 1024, 2048)])
+def test_streams_of_their_own(gpu, M, cols, outs):
+    ds = [make(M, cols, [outs], 5, 16, "f16", "whole", 31 + i) for i in range(3)]
     refs = [reference(d)[0] for d in ds]
     ads = [gpu.Adapters(d["A"], d["B"], ranks=d["ranks"], scales=d["scales"]) for d in ds]
-    wss = [gpu.adapter_workspace(ad, 70) for ad in ads]
-    plans = [gpu.AdapterPlan(70, 5) for _ in ads]
-    Ys = [torch.empty(70, 300, device="cuda") for _ in ads]
+    wss = [gpu.adapter_workspace(ad, M) for ad in ads]
+    plans = [gpu.AdapterPlan(M, 5) for _ in ads]
+    Ys = [torch.empty(M, outs, device="cuda") for _ in ads]
     streams = [torch.cuda.Stream() for _ in ads]
     torch.cuda.synchronize()
     for _ in range(10):
