@@ -401,6 +401,176 @@ block_norm_stream_kernel(const __grid_constant__ NormArgs p, int M) {
   }
 }
 
+// Many rows that are not aligned for groups of four: each row comes into shared
+// memory as the 16-byte words it lies across, and every thread takes elements a
+// CTA's width apart from there, E of them.  The copies of the next row go out as
+// soon as all threads have taken this one (the barrier inside a sum tells).
+template <bool H32, int E>
+__global__ void __launch_bounds__(kStreamThreads, 2)
+block_norm_ragged_kernel(const __grid_constant__ NormArgs p, int M) {
+  extern __shared__ __align__(16) unsigned char shared[];
+  float(*red)[4][32] = reinterpret_cast<float(*)[4][32]>(shared);  // [2]: sums of this row and the next
+  const seedlm_norm& nm = p.nm;
+  const int cols = nm.cols, tid = threadIdx.x;
+  constexpr int HB = H32 ? 4 : 2;
+  const bool pre = p.x && nm.pre, post = p.y && nm.post, gates = p.y && p.gate;
+  const bool gate_row = gates && p.ldg != 0 && nm.dtype != SEEDLM_F32;  // others are read when used
+  unsigned char* y_image = shared + kStreamSums;
+  unsigned char* h_image = y_image + (cols * 4 + 47) / 16 * 16;
+  unsigned char* g_image = h_image + (cols * HB + 47) / 16 * 16;
+  // Row m of a matrix of M rows, `size` bytes an element.
+  auto fetch = [&](unsigned char* image, const void* matrix, int64_t ld, int size, int64_t m) {
+    const unsigned char* first = static_cast<const unsigned char*>(matrix);
+    const unsigned char* end = first + ((M - 1) * ld + cols) * size;
+    const unsigned char* row = first + m * ld * size;
+    const int lead = (int)(reinterpret_cast<uintptr_t>(row) & 15), words = (lead + cols * size + 15) / 16;
+    const unsigned char* from = row - lead;
+    for (int c = tid; c < words; c += kStreamThreads) {
+      if (from + 16 * c >= first && from + 16 * c + 16 <= end) {
+        copy_async<16>(image + 16 * c, from + 16 * c);
+      } else {  // a word that leaves the matrix: what of it is in the row
+        for (int o = 0; o < 16; o += 2)
+          if (16 * c + o >= lead && 16 * c + o < lead + cols * size)
+            *reinterpret_cast<uint16_t*>(image + 16 * c + o) = *reinterpret_cast<const uint16_t*>(from + 16 * c + o);
+      }
+    }
+  };
+  auto image_of = [](unsigned char* image, const void* matrix, int64_t ld, int size, int64_t m) {
+    return image + ((reinterpret_cast<uintptr_t>(matrix) + m * ld * size) & 15);
+  };
+  auto fetch_y = [&](int64_t m) {
+    if (p.y && m < M) fetch(y_image, p.y, p.ldy, 4, m);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto fetch_rest = [&](int64_t m) {
+    if (p.h && m < M) fetch(h_image, p.h, p.ldh, HB, m);
+    if (gate_row && m < M) fetch(g_image, p.gate, p.ldg, 2, m);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto index = [&](int e) { return tid + kStreamThreads * e; };
+  const float inv = 1.f / cols;
+  // As normalise(), over this mapping; `taken` runs after the first barrier.
+  auto normalised = [&](float (&v)[E], float* sums, auto taken) {
+    bool told = false;
+    if (nm.kind == SEEDLM_NORM_LAYER) {
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) s += v[e];
+      const float mean = block_sum(s, sums) * inv;
+      taken();
+      told = true;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = index(e) < cols ? v[e] - mean : 0.f;
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s = fmaf(v[e], v[e], s);
+    const float rstd = rsqrtf(block_sum(s, sums + 32) * inv + nm.eps);
+    if (!told) taken();
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] *= rstd;
+  };
+  // v <- f(v, a) with a's elements of this thread; all loads before the first
+  // use, the type looked at once.  Beyond the row its last element stands in.
+  auto with = [&](float (&v)[E], const void* a, int dtype, auto f) {
+    if (dtype == SEEDLM_F32) {
+      float t[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) t[e] = static_cast<const float*>(a)[min(index(e), cols - 1)];
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = f(v[e], t[e]);
+    } else {
+      uint16_t t[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) t[e] = static_cast<const uint16_t*>(a)[min(index(e), cols - 1)];
+      if (dtype == SEEDLM_BF16) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = f(v[e], __uint_as_float((uint32_t)t[e] << 16));
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = f(v[e], __half2float(__ushort_as_half(t[e])));
+      }
+    }
+  };
+  auto weighed = [&](float (&v)[E], const void* w, const void* b) {
+    if (w) with(v, w, nm.dtype, [&](float v, float w) { return v * (nm.weight_offset + w); });
+    if (b) with(v, b, nm.dtype, [](float v, float b) { return v + b; });
+  };
+  // Beyond the row: zeros, as the sums need them.
+  auto cut = [&](float (&v)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (index(e) >= cols) v[e] = 0.f;
+  };
+  auto put = [&](void* to, int64_t row, int dtype, const float (&v)[E]) {
+    if (dtype == SEEDLM_F32) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (index(e) < cols) static_cast<float*>(to)[row + index(e)] = v[e];
+    } else if (dtype == SEEDLM_BF16) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (index(e) < cols) static_cast<__nv_bfloat16*>(to)[row + index(e)] = __float2bfloat16_rn(v[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (index(e) < cols) static_cast<__half*>(to)[row + index(e)] = __float2half_rn(v[e]);
+    }
+  };
+  grid_launch_dependents();
+  grid_wait();
+  fetch_y(blockIdx.x);
+  fetch_rest(blockIdx.x);
+  int parity = 0;
+  for (int64_t m = blockIdx.x; m < M; m += gridDim.x, parity ^= 1) {
+    float v[E];
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();
+    if (p.y) {
+      const float* y = reinterpret_cast<const float*>(image_of(y_image, p.y, p.ldy, 4, m));
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = index(e) < cols ? y[index(e)] : 0.f;
+    }
+    auto next_y = [&]() { fetch_y(m + gridDim.x); };
+    if (post) {
+      normalised(v, red[parity][0], next_y);
+      weighed(v, nm.w_post, nm.b_post);
+    } else {
+      __syncthreads();
+      next_y();
+    }
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();
+    if (gates) {
+      const void* g = gate_row ? image_of(g_image, p.gate, p.ldg, 2, m)
+                               : static_cast<const unsigned char*>(p.gate) + m * p.ldg * (nm.dtype == SEEDLM_F32 ? 4 : 2);
+      with(v, g, nm.dtype, [](float v, float g) { return v * g; });
+    }
+    if (p.h) {
+      if (!p.y) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = 0.f;
+      }
+      with(v, image_of(h_image, p.h, p.ldh, HB, m), H32 ? SEEDLM_F32 : p.h_dtype,
+           [&](float v, float h) { return fmaf(nm.y_scale, v, nm.h_scale * h); });
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] *= nm.y_scale;
+    }
+    cut(v);
+    auto next_rest = [&]() { fetch_rest(m + gridDim.x); };
+    if (p.h_out) put(p.h_out, m * p.ldho, H32 ? SEEDLM_F32 : p.h_dtype, v);
+    if (pre) {
+      normalised(v, red[parity][2], next_rest);
+      weighed(v, nm.w_pre, nm.b_pre);
+    } else {
+      __syncthreads();
+      next_rest();
+    }
+    if (p.x) put(p.x, m * p.ldx, p.x_dtype, v);
+  }
+}
+
 // Rows too wide for the registers of a CTA: the row is read again for every
 // step.
 constexpr int kWideThreads = 1024;
@@ -543,6 +713,27 @@ int launch_stream(const NormArgs& p, int M, cudaStream_t stream, const DeviceInf
   return launch_pdl(kernel, std::min<int64_t>(M, (int64_t)ctas * dev.num_sms), threads, (size_t)smem, stream, p, M);
 }
 
+template <bool H32, int E>
+int launch_ragged(const NormArgs& p, int M, cudaStream_t stream, const DeviceInfo& dev) {
+  const int cols = p.nm.cols;
+  const int smem = kStreamSums + (cols * 4 + 47) / 16 * 16 + (cols * (H32 ? 4 : 2) + 47) / 16 * 16 +
+                   (p.y && p.gate && p.ldg != 0 ? (cols * 2 + 47) / 16 * 16 : 0);
+  auto kernel = block_norm_ragged_kernel<H32, E>;
+  const int rc = allow_max_smem((const void*)kernel, dev);
+  if (rc) return rc;
+  const int ctas = std::max(1, std::min(2, 227 * 1024 / (smem + 1024)));
+  return launch_pdl(kernel, std::min(M, ctas * dev.num_sms), kStreamThreads, (size_t)smem, stream, p, M);
+}
+
+template <bool H32>
+int launch_ragged_of(const NormArgs& p, int M, cudaStream_t stream, const DeviceInfo& dev) {
+  const int each = (p.nm.cols + kStreamThreads - 1) / kStreamThreads;
+  return each <= 4    ? launch_ragged<H32, 4>(p, M, stream, dev)
+         : each <= 12 ? launch_ragged<H32, 12>(p, M, stream, dev)
+         : each <= 20 ? launch_ragged<H32, 20>(p, M, stream, dev)
+                      : launch_ragged<H32, 32>(p, M, stream, dev);
+}
+
 template <int ACT>
 int launch_glu_act(int M, int cols, const float* GU, int64_t ldgu, void* X, int64_t ldx, int x_dtype,
                    cudaStream_t stream) {
@@ -568,8 +759,9 @@ int launch_block_norm(const seedlm_norm& nm, int M, const float* y, int64_t ldy,
                    rows_of_four(nm.b_pre, 0, nm.dtype);
   // Few rows: as many threads as there are, for the latency of one row.  Many:
   // fewer threads with more of a row each, and the next row on its way.
-  if (vec && M > 2 * dev.num_sms && groups <= kStreamGroups * kStreamThreads) {
+  if (M > 2 * dev.num_sms && groups <= kStreamGroups * kStreamThreads) {
     const bool h32 = (h || h_out) && h_dtype == SEEDLM_F32;
+    if (!vec) return h32 ? launch_ragged_of<true>(p, M, stream, dev) : launch_ragged_of<false>(p, M, stream, dev);
     // The one 16-bit type of the call, if it has one.
     int t16 = x ? x_dtype : SEEDLM_F32;
     for (int t : {h || h_out ? h_dtype : SEEDLM_F32, nm.dtype})
