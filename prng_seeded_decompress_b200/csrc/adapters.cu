@@ -1349,13 +1349,15 @@ ShrinkShape shrink_shape(const seedlm_adapters& ad, int M, const DeviceInfo& dev
     clusters *= sh.groups;
     round = ShrinkTallLayout<true>::kStages * ShrinkTallLayout<true>::kCols / kStep;
   }
-  // Low: enough CTAs for three on each SM.  Tall: no more than the two that fit
+  // Low: about one and a half CTAs for each SM, as many again for the last
+  // doubling (37 rows, 20 adapters, fused q, k, v of 4096 columns: 9.1 us with 300
+  // CTAs, 11.7 with 600).  Tall: no more than the two that fit
   // one (a second round of CTAs costs more than their shorter parts save; 4096
   // rows, 8192 columns: 32 us in one round of 4 parts, 42 in two of 8).
   const int64_t steps = (ad.cols + kStep - 1) / kStep;
   sh.splits = 1;
   while (sh.splits < kMaxSplits && steps >= 2 * sh.splits * round &&
-         (sh.low ? sh.splits * clusters < 3 * dev.num_sms : sh.splits * clusters <= dev.num_sms))
+         (sh.low ? 2 * sh.splits * clusters < 3 * dev.num_sms : sh.splits * clusters <= dev.num_sms))
     sh.splits *= 2;
   // Parts begin at whole stages of either form.
   sh.split_cols = (int)(((steps + sh.splits - 1) / sh.splits + 1) / 2 * 2 * kStep);
@@ -1413,16 +1415,19 @@ int launch_products(ApplyArgs& p, const ShrinkShape& sh, int64_t tiles, cudaStre
   else
     rc = launch_shrink_tall<BF16, WIDE>(p, tiles, sh.splits, stream, dev);
   if (rc) return rc;
-  // Chunks of outputs.  Low tiles, a CTA each: as long as they can be (a CTA
-  // fetches its S once) with enough CTAs left for several rounds of the GPU, at
-  // least one round of the CTA's warps.  Tall tiles: the outputs of one product.
+  // Chunks of outputs.  Low tiles, a CTA each: long enough that a CTA's start is
+  // paid for, short enough that there are five CTAs for each SM, up to 12 rounds
+  // of the CTA's warps (64 rows of their own adapters, rank 64: 187 us on
+  // 28672+28672 outputs with one round, 114 with 12, 116 with 16; rank 16 on
+  // 8192: 23 with one, 19 with 6, 23 with 16).  Tall tiles: the outputs of one
+  // product.
   int64_t total = 0;
   for (int s = 0; s < p.ad.slices; ++s) total += p.ad.rows[s];
   p.chunk_rows = kTallOutputs;
   if (low) {
     const int round = 32 * kLowWarps;
-    const int64_t rounds = total * tiles / ((int64_t)round * 12 * dev.num_sms);
-    p.chunk_rows = (int)(rounds < 1 ? 1 : rounds > 16 ? 16 : rounds) * round;
+    const int64_t rounds = (total * tiles - 1) / ((int64_t)round * 5 * dev.num_sms) + 1;
+    p.chunk_rows = (int)std::min<int64_t>(rounds, 12) * round;
   }
   int64_t chunks = 0;
   int at = 0;
