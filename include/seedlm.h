@@ -287,10 +287,10 @@ enum { SEEDLM_MAX_SLICES = 4, SEEDLM_MAX_RANK = 256, SEEDLM_MAX_ADAPTERS = 1024 
 typedef struct seedlm_adapters {
   int32_t n;          /* adapters, 1..SEEDLM_MAX_ADAPTERS                        */
   int32_t rank;       /* largest rank, 1..SEEDLM_MAX_RANK                        */
-  int32_t cols;       /* inputs of the projection, >= 0                          */
+  int32_t cols;       /* inputs of the projection, 0..2^30                       */
   int32_t slices;     /* 1..SEEDLM_MAX_SLICES                                    */
   int32_t dtype;      /* of A and B, and of X: SEEDLM_F16 or SEEDLM_BF16         */
-  int32_t rows[4];    /* outputs of each slice, >= 0 (their sum below 2^31)      */
+  int32_t rows[4];    /* outputs of each slice, >= 0 (their sum at most 2^30)    */
   const void* A[4];
   const void* B[4];
   int64_t a_adapter[4], a_row[4], b_adapter[4], b_row[4];  /* >= 0               */
@@ -374,7 +374,8 @@ SEEDLM_API int seedlm_block_norm(const seedlm_norm* nm, int32_t M, const float* 
 
 /* The gated activation between a fused gate+up product and the down product:
  * X[m][f] = act(GU[m][f]) * GU[m][cols + f], GU M x 2 cols fp32, X M x cols
- * SEEDLM_F16 or SEEDLM_BF16, computed in fp32 and rounded once.
+ * SEEDLM_F16 or SEEDLM_BF16, computed in fp32 and rounded once; cols at most
+ * 2^30.
  *   SILU: g / (1 + e^-g)   GELU: g/2 (1 + erf(g / sqrt 2))
  *   GELU_TANH: g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
 enum { SEEDLM_SILU = 0, SEEDLM_GELU = 1, SEEDLM_GELU_TANH = 2 };

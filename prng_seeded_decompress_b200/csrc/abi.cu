@@ -114,6 +114,8 @@ int64_t gemm_any_workspace(const seedlm_format& f, int M, const DeviceInfo& dev)
   return need;
 }
 
+constexpr int kMaxWidth = 1 << 30;  // columns that the kernels below count in 32 bits
+
 bool act_dtype(int t) { return t == SEEDLM_F16 || t == SEEDLM_BF16; }
 bool any_dtype(int t) { return act_dtype(t) || t == SEEDLM_F32; }
 uintptr_t bytes_of(int t) { return t == SEEDLM_F32 ? 4 : 2; }
@@ -133,7 +135,7 @@ int check_adapters(const seedlm_adapters* ad, int64_t* total) {
     if (ad->rows[s] > 0 && (!ad->B[s] || !aligned(ad->B[s], 2))) return SEEDLM_EINVAL;
     *total += ad->rows[s];
   }
-  if (*total > INT32_MAX) return SEEDLM_EINVAL;
+  if (*total > kMaxWidth || ad->cols > kMaxWidth) return SEEDLM_EUNSUPPORTED;
   if ((ad->ranks && !aligned(ad->ranks, 4)) || (ad->scales && !aligned(ad->scales, 4)))
     return SEEDLM_EINVAL;
   return SEEDLM_OK;
@@ -399,6 +401,7 @@ int seedlm_glu(int32_t M, int32_t cols, int act, const float* GU, int64_t ldgu, 
                int64_t ldx, int x_dtype, seedlm_stream stream) {
   if (M < 0 || cols < 0 || act < SEEDLM_SILU || act > SEEDLM_GELU_TANH) return SEEDLM_EINVAL;
   if (!act_dtype(x_dtype)) return SEEDLM_EINVAL;
+  if (cols > kMaxWidth) return SEEDLM_EUNSUPPORTED;
   if (M == 0 || cols == 0) return SEEDLM_OK;
   if (!GU || !aligned(GU, 4) || ldgu < 2 * (int64_t)cols) return SEEDLM_EINVAL;
   if (!X || !aligned(X, 2) || ldx < cols) return SEEDLM_EINVAL;

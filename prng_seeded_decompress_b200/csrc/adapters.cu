@@ -278,7 +278,7 @@ struct ApplyArgs {
 // The plan's head, {M, n, tiles with an adapter, tiles}, with no tiles at all if
 // it does not belong to this call.
 __device__ __forceinline__ int4 plan_head(const ApplyArgs& p) {
-  int4 head = *p.head;
+  int4 head = __ldcg(p.head);
   if (head.x != p.M || head.y != p.ad.n) {
     if (threadIdx.x == 0) atomicOr(&g_plan_mismatch, 1u);
     head.z = head.w = 0;
@@ -289,12 +289,12 @@ __device__ __forceinline__ int4 plan_head(const ApplyArgs& p) {
 // Tile t {adapter or -1, first, rows, 0}; t below the plan's room, whether the
 // plan has so many or not.
 __device__ __forceinline__ int4 plan_tile(const ApplyArgs& p, int64_t t) {
-  return p.tiles[t];
+  return __ldcg(p.tiles + t);
 }
 
 __device__ __forceinline__ int rank_of(const seedlm_adapters& ad, int a) {
   if (a < 0) return 0;
-  return ad.ranks ? max(0, min(ad.ranks[a], ad.rank)) : ad.rank;
+  return ad.ranks ? max(0, min(__ldcg(ad.ranks + a), ad.rank)) : ad.rank;
 }
 
 template <bool BF16>
@@ -416,6 +416,32 @@ __device__ __forceinline__ uint4 load_unit(const Unit& u) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// In a checked build: `have` elements from `at` on if they lie in the matrix that
+// the call describes, else none and the flag; otherwise `have`.
+__device__ __forceinline__ int checked_x(const ApplyArgs& p, const uint16_t* at, int have) {
+  SEEDLM_CHECK_ONLY(const int64_t i = at - p.X; if (have > 0 && (i < 0 ||
+      !SEEDLM_IN_BOUNDS(g_check_flag, i + have - 1, (p.M - 1) * p.ldx + p.ad.cols))) return 0;)
+  return have;
+}
+__device__ __forceinline__ int checked_a(const ApplyArgs& p, int s, const uint16_t* at, int have) {
+  SEEDLM_CHECK_ONLY(const int64_t i = at - static_cast<const uint16_t*>(p.ad.A[s]); if (have > 0 && (i < 0 ||
+      !SEEDLM_IN_BOUNDS(g_check_flag, i + have - 1, (p.ad.n - 1) * p.ad.a_adapter[s] +
+                                                      (p.ad.rank - 1) * p.ad.a_row[s] + p.ad.cols))) return 0;)
+  return have;
+}
+__device__ __forceinline__ int checked_b(const ApplyArgs& p, int s, const uint16_t* at, int have) {
+  SEEDLM_CHECK_ONLY(const int64_t i = at - static_cast<const uint16_t*>(p.ad.B[s]); if (have > 0 && (i < 0 ||
+      !SEEDLM_IN_BOUNDS(g_check_flag, i + have - 1, (p.ad.n - 1) * p.ad.b_adapter[s] +
+                                                      (p.ad.rows[s] - 1) * p.ad.b_row[s] + p.ad.rank))) return 0;)
+  return have;
+}
+// Whether outputs at .. at + n - 1 of base or Y lie in it.
+__device__ __forceinline__ bool checked_y(const ApplyArgs& p, const float* at, const float* of, int64_t ld, int n) {
+  SEEDLM_CHECK_ONLY(const int64_t i = at - of; const int64_t width = p.slice_at[p.ad.slices - 1] + p.ad.rows[p.ad.slices - 1];
+                    if (i < 0 || !SEEDLM_IN_BOUNDS(g_check_flag, i + n - 1, (p.M - 1) * ld + width)) return false;)
+  return true;
+}
+
 // ---- the first kernel's end: the cluster's sums to S
 
 __device__ __forceinline__ float2 load_of_cta(const float* mine, uint32_t cta) {
@@ -504,7 +530,7 @@ __device__ __forceinline__ void store_sums(const ApplyArgs& p, const float* sums
 // coming into shared memory; a lane copies exactly what it will itself read, so
 // the ring needs no barrier.
 template <int RB>
-constexpr int kShrinkLowStages = RB == 4 ? 4 : 6;
+constexpr int kShrinkLowStages = RB == 4 ? 5 : 6;
 template <int RB, bool WIDE>
 constexpr int kShrinkLowSmem = kLowWarps * kShrinkLowStages<RB> * (2 * RB + 1) * (WIDE ? 512 : 1024);
 
@@ -524,9 +550,9 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
   if (t >= head.z) return;
   const int a = tile.x, first = tile.y, count = tile.z;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
-  const int row = g < count ? p.plan[first + g] : -1;
+  const int row = g < count ? __ldcg(p.plan + first + g) : -1;
   const int r0 = group * R, rank = rank_of(p.ad, a) - r0;  // of this group
-  const float scale = p.ad.scales ? p.ad.scales[a] : 1.f;
+  const float scale = p.ad.scales ? __ldcg(p.ad.scales + a) : 1.f;
   if (rank <= 0) return;
   const int k0 = (int)cluster_rank() * p.split_cols, k1 = min(p.ad.cols, k0 + p.split_cols);
   const int blocks = min(RB, (rank + 15) / 16);
@@ -538,6 +564,7 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
   const uint16_t* x = p.X + (have_x ? row * p.ldx : 0) + k_first;
   const uint16_t* A = static_cast<const uint16_t*>(p.ad.A[s]) + a * p.ad.a_adapter[s] + r0 * a_row + k_first;
   unsigned char* ring = smem + warp * kStages * kStageBytes + lane * 16;
+  if (!SEEDLM_IN_BOUNDS(g_check_flag, (kShrinkLowSmem<RB, WIDE>)-1, seedlm_dynamic_smem_bytes())) return;
   const int steps = k1 > k0 ? max(0, ((k1 - k0 + kStep - 1) / kStep - warp + kLowWarps - 1) / kLowWarps) : 0;
   // Every copy of a step is made, those of rows that are not there with no
   // bytes read and zeros written, so what is multiplied below needs no checks;
@@ -554,18 +581,18 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
 #pragma unroll
             for (int j = 2 * b; j < 2 * b + 2; ++j) {
               const int r = 8 * j + g;
-              copy16(to + j * kUnit, A + (r < rank ? r : 0) * a_row, r < rank ? 2 * have : 0);
+              copy16(to + j * kUnit, A + (r < rank ? r : 0) * a_row, 2 * checked_a(p, s, A + r * a_row, r < rank ? have : 0));
             }
           }
-        copy16(to + 2 * RB * kUnit, x, have_x ? 2 * have : 0);
+        copy16(to + 2 * RB * kUnit, x, 2 * checked_x(p, x, have_x ? have : 0));
       } else {
 #pragma unroll 1
         for (int j = 0; j < 2 * blocks; ++j) {
           const int r = 8 * j + g;
-          copy_raw(Unit{to + j * kUnit, A + r * a_row, r < rank ? have : 0, r * a_row + k,
+          copy_raw(Unit{to + j * kUnit, A + r * a_row, checked_a(p, s, A + r * a_row, r < rank ? have : 0), r * a_row + k,
                         (rank - 1 - r) * a_row + p.ad.cols - k}, 512);
         }
-        copy_raw(Unit{to + 2 * RB * kUnit, x, have_x ? have : 0, row * p.ldx + k,
+        copy_raw(Unit{to + 2 * RB * kUnit, x, checked_x(p, x, have_x ? have : 0), row * p.ldx + k,
                       (p.M - 1 - row) * p.ldx + p.ad.cols - k}, 512);
       }
       A += kLowWarps * kStep;
@@ -703,7 +730,7 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
         if (s < p.ad.slices && r < rank)
           src[i] = static_cast<const uint16_t*>(p.ad.A[s]) + a * p.ad.a_adapter[s] + r * p.ad.a_row[s];
       } else {
-        const int m = row - L::kSlots < count ? p.plan[first + row - L::kSlots] : -1;
+        const int m = row - L::kSlots < count ? __ldcg(p.plan + first + row - L::kSlots) : -1;
         if (m >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, m, p.M)) src[i] = p.X + m * p.ldx;
       }
       there |= (unsigned)(src[i] != nullptr) << i;
@@ -711,6 +738,9 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
         for (int st = 0; st < L::kStages; ++st)
           *reinterpret_cast<uint4*>(smem + st * L::kStageBytes + i * 2048 + place) = make_uint4(0u, 0u, 0u, 0u);
     }
+    auto checked = [&](int i, const uint16_t* at, int have) {
+      return 16 * i < L::kSlots ? checked_a(p, (group * L::kSlots + row0 + 16 * i) / p.slots, at, have) : checked_x(p, at, have);
+    };
     auto fetch = [&](int step) {
       if (step < steps) {
         const int k = k0 + step * L::kCols + 8 * unit, have = max(0, min(8, k1 - k));
@@ -718,12 +748,12 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
           unsigned char* to = smem + step % L::kStages * L::kStageBytes + place;
 #pragma unroll
           for (int i = 0; i < kMine; ++i)
-            if (there >> i & 1) copy16(to + i * 2048, src[i] + k, 2 * have);
+            if (there >> i & 1) copy16(to + i * 2048, src[i] + k, 2 * checked(i, src[i] + k, have));
         } else {
           unsigned char* to = smem + L::kRaw + step % L::kAhead * L::kRawBytes + tid * 16;
 #pragma unroll
           for (int i = 0; i < kMine; ++i)  // within the row: its neighbours are not always the same matrix's
-            if (there >> i & 1) copy_raw(Unit{to + i * 4096, src[i] + k, have, k, p.ad.cols - k}, 2048);
+            if (there >> i & 1) copy_raw(Unit{to + i * 4096, src[i] + k, checked(i, src[i] + k, have), k, p.ad.cols - k}, 2048);
         }
       }
       copies_commit();
@@ -781,7 +811,7 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
       for (int r = 0; r < 16; ++r) sums[(16 * c + r) * L::kSumStride + tid] = v[r];
     }
     store_sums<BF16, L::kSlots>(p, sums, L::kSumStride, first, count, rank, group * L::kSlots,
-                                p.ad.scales ? p.ad.scales[a] : 1.f);
+                                p.ad.scales ? __ldcg(p.ad.scales + a) : 1.f);
   }
   if (!ok && lane == 0) atomicOr(&g_wait_error, 1u);
   tc::fence_before_sync();
@@ -795,7 +825,8 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
 // ---- the second kernel
 
 // A lane's four outputs of one row: to = from + d.
-__device__ __forceinline__ void add4_slow(float* to, const float* from, float4 d, int left) {
+__device__ __forceinline__ void add4_slow(const ApplyArgs& p, float* to, const float* from, float4 d, int left) {
+  if (left <= 0 || !checked_y(p, to, p.Y, p.ldy, min(left, 4)) || !checked_y(p, from, p.base, p.ldb, min(left, 4))) return;
   const float dv[4] = {d.x, d.y, d.z, d.w};
   float b[4];
 #pragma unroll
@@ -868,7 +899,7 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
   float* to[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const int m = 2 * q + e < x.count ? p.plan[x.first + 2 * q + e] : -1;
+    const int m = 2 * q + e < x.count ? __ldcg(p.plan + x.first + 2 * q + e) : -1;
     const bool ok = m >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, m, p.M);
     from[e] = ok ? p.base + m * p.ldb + p.slice_at[x.s] + 4 * g : nullptr;
     to[e] = ok ? p.Y + m * p.ldy + p.slice_at[x.s] + 4 * g : nullptr;
@@ -897,9 +928,9 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
         const int n = fetch_n + 4 * g + j;
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
-          const int wanted = whole || n < x.c1 ? have[c] : 0;
           unsigned char* to = into + (4 * c + j) * 512;
           const uint16_t* from = b + kStep * c;
+          const int wanted = checked_b(p, x.s, from, whole || n < x.c1 ? have[c] : 0);
           if (WIDE) {
             copy16_short(to, from, 2 * wanted);
           } else if (eights) {
@@ -918,7 +949,9 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
         if (vec_y && whole) {
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            if (from[e]) copy16(into + kItemBytes - 1024 + e * 512, from[e] + fetch_n, 16);
+            if (from[e])
+              copy16(into + kItemBytes - 1024 + e * 512, from[e] + fetch_n,
+                     checked_y(p, from[e] + fetch_n, p.base, p.ldb, 4) ? 16 : 0);
         }
         b_next += kRound * b_row - 64 * groups;
         fetch_n += kRound;
@@ -1003,9 +1036,10 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
         const float4 d = make_float4(total[0][e], total[0][2 + e], total[1][e], total[1][2 + e]);
         if (whole) {
           const float4 b = *reinterpret_cast<const float4*>(item_at + kItemBytes - 1024 + e * 512);
-          *reinterpret_cast<float4*>(to[e] + n0) = make_float4(b.x + d.x, b.y + d.y, b.z + d.z, b.w + d.w);
+          if (checked_y(p, to[e] + n0, p.Y, p.ldy, 4))
+            *reinterpret_cast<float4*>(to[e] + n0) = make_float4(b.x + d.x, b.y + d.y, b.z + d.z, b.w + d.w);
         } else {
-          add4_slow(to[e] + n0, from[e] + n0, d, x.c1 - n0 - 4 * g);
+          add4_slow(p, to[e] + n0, from[e] + n0, d, x.c1 - n0 - 4 * g);
         }
       }
 #pragma unroll
@@ -1100,7 +1134,7 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
     const bool products = rank > 0;
     __syncthreads();  // the tile before is done with shared memory
     if (tid < T) {
-      const int m = tid < count ? p.plan[first + tid] : 0;
+      const int m = tid < count ? __ldcg(p.plan + first + tid) : 0;
       const bool in = SEEDLM_IN_BOUNDS(g_check_flag, m, p.M);
       from_row[tid] = (in ? m * p.ldb : 0) + p.slice_at[s];
       to_row[tid] = (in ? m * p.ldy : 0) + p.slice_at[s];
@@ -1116,7 +1150,7 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
         auto unit_of = [&](int u) {
           const int j = u / 2, h = u % 2, at = n + 32 * j + h;
           return Unit{to + (h * NB + b) * 128 * 128 + j * 16 * 128, src + 64 * b + (32 * j + h) * b_row,
-                      at < rows ? have : 0, at * b_row + 64 * b + 8 * unit,
+                      checked_b(p, s, src + 64 * b + (32 * j + h) * b_row, at < rows ? have : 0), at * b_row + 64 * b + 8 * unit,
                       (rows - 1 - at) * b_row + rank - 64 * b - 8 * unit};
         };
         if (WIDE) {
@@ -1203,12 +1237,14 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
       const float* from = p.base + n;
       if (pairs && count >= kQ * (q + 1) && c0 + (i + 1) * kOut <= rows) {
 #pragma unroll
-        for (int r = 0; r < kQ; ++r) ahead[r] = __ldcs(reinterpret_cast<const float2*>(from + from_row[kQ * q + r]));
+        for (int r = 0; r < kQ; ++r)
+          if (checked_y(p, from + from_row[kQ * q + r], p.base, p.ldb, 2))
+            ahead[r] = __ldcs(reinterpret_cast<const float2*>(from + from_row[kQ * q + r]));
       } else {
 #pragma unroll
         for (int r = 0; r < kQ; ++r) {
           const float* at = from + from_row[kQ * q + r];
-          const bool in = kQ * q + r < count;
+          const bool in = kQ * q + r < count && (n >= rows || checked_y(p, at, p.base, p.ldb, min(2, rows - n)));
           ahead[r].x = in && n < rows ? __ldcg(at) : 0.f;
           ahead[r].y = in && n + 1 < rows ? __ldcg(at + 1) : 0.f;
         }
@@ -1255,12 +1291,14 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
         if (!ok) continue;
         if (pairs && count >= kQ * (q + 1) && c0 + (i + 1) * kOut <= rows) {
 #pragma unroll
-          for (int r = 0; r < kQ; ++r) __stcs(reinterpret_cast<float2*>(to + to_row[kQ * q + r]), v[r]);
+          for (int r = 0; r < kQ; ++r)
+            if (checked_y(p, to + to_row[kQ * q + r], p.Y, p.ldy, 2))
+              __stcs(reinterpret_cast<float2*>(to + to_row[kQ * q + r]), v[r]);
         } else {
 #pragma unroll
           for (int r = 0; r < kQ; ++r) {
             float* at = to + to_row[kQ * q + r];
-            const bool in = kQ * q + r < count;
+            const bool in = kQ * q + r < count && (n >= rows || checked_y(p, at, p.Y, p.ldy, min(2, rows - n)));
             if (in && n < rows) at[0] = v[r].x;
             if (in && n + 1 < rows) at[1] = v[r].y;
           }

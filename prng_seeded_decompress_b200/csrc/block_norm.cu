@@ -59,6 +59,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 
 struct NormArgs {
   seedlm_norm nm;
+  int M;
   const float* y;
   int64_t ldy;
   const void* gate;
@@ -233,6 +234,7 @@ __global__ void __launch_bounds__(kRowThreads) block_norm_kernel(const __grid_co
   const int cols = nm.cols;
   const int64_t m = blockIdx.x;
   using S = Share<NV, VEC>;
+  if (!SEEDLM_IN_BOUNDS(g_check_flag, m, p.M)) return;
   grid_launch_dependents();
   grid_wait();
   float v[NV][4], h[NV][4];
@@ -305,6 +307,9 @@ block_norm_stream_kernel(const __grid_constant__ NormArgs p, int M) {
   unsigned char* y_at = shared + kStreamSums + threadIdx.x * 16;
   unsigned char* h_at = shared + kStreamSums + NV * threads * 16 + threadIdx.x * HB;
   unsigned char* g_at = shared + kStreamSums + NV * threads * (16 + HB) + threadIdx.x * 8;
+  if (!SEEDLM_IN_BOUNDS(g_check_flag, kStreamSums + NV * threads * (16 + HB + (gate_row ? 8 : 0)) - 1,
+                        seedlm_dynamic_smem_bytes()))
+    return;
   auto fetch_y = [&](int64_t m) {
     if (p.y && m < M) {
       const float* from = p.y + m * p.ldy;
@@ -418,6 +423,9 @@ block_norm_ragged_kernel(const __grid_constant__ NormArgs p, int M) {
   unsigned char* y_image = shared + kStreamSums;
   unsigned char* h_image = y_image + (cols * 4 + 47) / 16 * 16;
   unsigned char* g_image = h_image + (cols * HB + 47) / 16 * 16;
+  if (!SEEDLM_IN_BOUNDS(g_check_flag, g_image - shared + (gate_row ? (cols * 2 + 47) / 16 * 16 : 0) - 1,
+                        seedlm_dynamic_smem_bytes()))
+    return;
   // Row m of a matrix of M rows, `size` bytes an element.
   auto fetch = [&](unsigned char* image, const void* matrix, int64_t ld, int size, int64_t m) {
     const unsigned char* first = static_cast<const unsigned char*>(matrix);
@@ -609,6 +617,7 @@ __global__ void __launch_bounds__(kWideThreads) block_norm_wide_kernel(const __g
   grid_launch_dependents();
   grid_wait();
   const int64_t m = blockIdx.x;
+  if (!SEEDLM_IN_BOUNDS(g_check_flag, m, p.M)) return;
   const seedlm_norm& nm = p.nm;
   Stats post{}, pre{};
   auto y = [&](int j) { return p.y[m * p.ldy + j]; };
@@ -749,7 +758,7 @@ int launch_glu_act(int M, int cols, const float* GU, int64_t ldgu, void* X, int6
 int launch_block_norm(const seedlm_norm& nm, int M, const float* y, int64_t ldy, const void* gate, int64_t ldg,
                       const void* h, int64_t ldh, void* h_out, int64_t ldho, int h_dtype, void* x, int64_t ldx,
                       int x_dtype, cudaStream_t stream, const DeviceInfo& dev) {
-  NormArgs p{nm, y, ldy, gate, ldg, h, ldh, h_out, ldho, h_dtype, x, ldx, x_dtype};
+  NormArgs p{nm, M, y, ldy, gate, ldg, h, ldh, h_out, ldho, h_dtype, x, ldx, x_dtype};
   const int cols = nm.cols, groups = (cols + 3) / 4;
   if (groups > 4 * kRowThreads) return launch_pdl(block_norm_wide_kernel, M, kWideThreads, 0, stream, p);
   const bool vec = cols % 4 == 0 && rows_of_four(y, ldy, SEEDLM_F32) && rows_of_four(gate, ldg, nm.dtype) &&

@@ -53,6 +53,7 @@ def _struct(sl, **kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(n=0), -1), (dict(rank=0), -1), (dict(cols=-1), -1), (dict(slices=0), -1), (dict(dtype=2), -1),
     (dict(n=1025), -2), (dict(rank=257), -2), (dict(slices=5), -2), (dict(rows=-1), -1),
+    (dict(cols=(1 << 30) + 1), -2), (dict(rows=(1 << 30) + 1), -2),
     (dict(A=0), -1), (dict(B=0), -1), (dict(A=0x1001), -1), (dict(B=0x2001), -1), (dict(a_adapter=-1), -1),
     (dict(a_row=-1), -1), (dict(b_adapter=-1), -1), (dict(b_row=-1), -1), (dict(ranks=0x3002), -1),
     (dict(scales=0x3002), -1),

@@ -69,7 +69,7 @@ def test_empty_norm_and_null(sl):
 @pytest.mark.parametrize("kw,code", [
     (dict(M=-1), -1), (dict(cols=-1), -1), (dict(act=3), -1), (dict(act=-1), -1), (dict(xt=2), -1), (dict(GU=None), -1),
     (dict(GU=0x1002), -1), (dict(ldgu=127), -1), (dict(X=None), -1), (dict(X=0x2001), -1), (dict(ldx=63), -1),
-    (dict(M=0), 0), (dict(cols=0), 0),
+    (dict(M=0), 0), (dict(cols=0), 0), (dict(cols=(1 << 30) + 1), -2),
 ])
 def test_bad_glu_calls_are_refused_before_cuda(sl, kw, code):
     a = dict(M=3, cols=64, act=0, GU=0x1000, ldgu=128, X=0x2000, ldx=64, xt=0)

@@ -16,7 +16,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-D, F, N, RANK = 264, 200, 5, 12
+N, RANK = 5, 12
 
 
 @pytest.fixture(scope="module")
@@ -31,10 +31,10 @@ def sl():
 
 
 class Step:
-    """The MLP half of a decoder layer over M rows."""
+    """The MLP half of a decoder layer over M rows, D wide, F inside."""
 
-    def __init__(self, sl, oracle_mod, M, dtype, C, P):
-        self.sl, self.M = sl, M
+    def __init__(self, sl, oracle_mod, M, dtype, C, P, D=264, F=200):
+        self.sl, self.M, self.F = sl, M, F
         self.dt = dt = torch.bfloat16 if dtype == "bf16" else torch.float16
         g = torch.Generator().manual_seed(M)
         rnd = lambda *s, std=1.0: torch.randn(s, generator=g) * std  # noqa: E731
@@ -117,7 +117,7 @@ class Step:
         rounded(self.x, ref, u * ref.abs())
         product(0, self.x, self.gu0)
         adapted(0, self.x, self.gu0, self.gu)
-        g, up = d(self.gu)[:, :F], d(self.gu)[:, F:]
+        g, up = d(self.gu)[:, :self.F], d(self.gu)[:, self.F:]
         rounded(self.act, g * torch.sigmoid(g) * up, 2.0 ** -21 * (g * up).abs())
         product(1, self.act, self.y0)
         adapted(1, self.act, self.y0, self.y)
@@ -133,10 +133,15 @@ class Step:
         return [t.clone() for t in (self.x, self.gu0, self.gu, self.act, self.y0, self.y, self.h2, self.x2)]
 
 
-@pytest.mark.parametrize("M,dtype,C,P", [(1, "bf16", 8, 3), (1, "f16", 12, 4), (3, "bf16", 12, 4), (17, "f16", 8, 3),
+#: 2048 rows of this width take the adapters' tensor-memory kernels, between
+#: products that take all of it.
+WIDE = dict(D=1032, F=1100)
+
+
+@pytest.mark.parametrize("M,dtype,C,P", [(2048, "bf16", 8, 3), (2048, "f16", 12, 4), (1, "bf16", 8, 3), (1, "f16", 12, 4), (3, "bf16", 12, 4), (17, "f16", 8, 3),
                                          (64, "bf16", 8, 3), (300, "bf16", 12, 4), (300, "f16", 8, 3)])
 def test_a_layers_mlp_half_stage_by_stage(sl, oracle_mod, M, dtype, C, P):
-    s = Step(sl, oracle_mod, M, dtype, C, P)
+    s = Step(sl, oracle_mod, M, dtype, C, P, **(WIDE if M == 2048 else {}))
     s.run()
     torch.cuda.synchronize()
     s.check()
@@ -149,9 +154,9 @@ def test_a_layers_mlp_half_stage_by_stage(sl, oracle_mod, M, dtype, C, P):
     assert all(torch.equal(a, b) for a, b in zip(first, s.outputs()))
 
 
-@pytest.mark.parametrize("M", [1, 20, 300])
+@pytest.mark.parametrize("M", [1, 20, 300, 2048])
 def test_the_same_step_captured_into_a_graph(sl, oracle_mod, M):
-    s = Step(sl, oracle_mod, M, "bf16", 8, 3)
+    s = Step(sl, oracle_mod, M, "bf16", 8, 3, **(WIDE if M == 2048 else {}))
     s.run()
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
@@ -159,7 +164,7 @@ def test_the_same_step_captured_into_a_graph(sl, oracle_mod, M):
         s.run()
     for seed in range(3):  # the graph follows its inputs, the batch's adapters among them
         gen = torch.Generator().manual_seed(seed)
-        s.h.copy_(torch.randn(M, D, generator=gen))
+        s.h.copy_(torch.randn(s.h.shape, generator=gen))
         s.ids.copy_(torch.randint(-1, N, (M,), generator=gen).to(torch.int32))
         g.replay()
         torch.cuda.synchronize()
