@@ -610,7 +610,9 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
     off[2 * RB] = off_of(x);
   }
   for (int i = 0; i < kStages - 1; ++i) fetch();
-  float acc[RB][4] = {};
+  // The tensor cores cut off what an addition leaves below the sum's last bit, so
+  // they only add up 8 steps; those sums are added in fp32, rounded.
+  float acc[RB][4] = {}, total[RB][4] = {};
   const unsigned char* from = ring;
   for (int step = 0; step < steps; ++step) {
     copies_wait<kStages - 2>();
@@ -631,6 +633,14 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
 #pragma unroll
       for (int b = 0; b < RB; ++b)
         if (b < blocks) mma_half<BF16>(half, acc[b], w[2 * b], w[2 * b + 1], v);
+    if (step % 8 == 7 || step == steps - 1)
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          total[b][e] += acc[b][e];
+          acc[b][e] = 0.f;
+        }
     read_k += kLowWarps * kStep;
     from = from == ring + (kStages - 1) * kStageBytes ? ring : from + kStageBytes;
     fetch();
@@ -645,7 +655,7 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
 #pragma unroll
   for (int b = 0; b < RB; ++b)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) red[(warp * R + 16 * b + 8 * (e / 2) + g) * 9 + 2 * q + e % 2] = acc[b][e];
+    for (int e = 0; e < 4; ++e) red[(warp * R + 16 * b + 8 * (e / 2) + g) * 9 + 2 * q + e % 2] = total[b][e];
   __syncthreads();
   for (int e = threadIdx.x; e < R * count; e += 32 * kLowWarps) {
     const int r = e % R, i = e / R;
@@ -662,12 +672,12 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
 // its CTAs one part of the columns, 64 at a time through a ring of shared-memory
 // stages.  Bound by the traffic from L2 (A again for every tile).  The tensor
 // cores cut off what an addition leaves below a sum's last bit, so the stages go
-// to four sums in turn, which are added in fp32, rounded.
+// to four sums in turn, which after every 32 stages are added up in fp32, rounded.
 // Rows that are not aligned to 16 bytes (not WIDE) come raw, nine words for 64
 // elements, and each thread shifts what it copied into place when it is there.
 template <bool WIDE>
 struct ShrinkTallLayout {
-  static constexpr int kThreads = 128, kStages = WIDE ? 4 : 2, kCols = 64, kSlots = 128, kSums = 4;
+  static constexpr int kThreads = 128, kStages = WIDE ? 4 : 2, kCols = 64, kSlots = 128, kSums = 4, kFlush = 32;
   static constexpr int kStageBytes = (kSlots + kTall) * 128;   // rows of A, then rows of X
   static constexpr int kAhead = 3;                             // stages of copies on their way
   static constexpr int kRawBytes = (kSlots + kTall) * 8 * 32;  // two words for each unit
@@ -763,6 +773,7 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
     auto wait_for = [&](int step) {
       ok = tc::mbar_wait_or_abort(bars + 8 * (step % L::kStages), (step / L::kStages) & 1, kTallWaitLimit, slot + 1) && ok;
     };
+    float total[kTall] = {};  // of slot tid
     for (int step = 0; step < steps; ++step) {
       copies_wait<L::kAhead - 1>();
       const int st = step % L::kStages;
@@ -779,37 +790,40 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
       tc::fence_proxy_async();
       __syncthreads();
       if (warp == 0) {
+        tc::fence_after_sync();
+        const int turn = step % L::kFlush;
         const uint64_t w = tc::smem_desc_sw128(tc::smem_u32(smem + st * L::kStageBytes));
         const uint64_t x = w + L::kSlots * 128 / 16;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          tc::mma_f16_ss_warp(tmem + step % L::kSums * kTall, w + 2 * k, x + 2 * k, idesc, step >= L::kSums || k > 0);
+          tc::mma_f16_ss_warp(tmem + turn % L::kSums * kTall, w + 2 * k, x + 2 * k, idesc, turn >= L::kSums || k > 0);
         tc::mma_commit_warp(bars + 8 * st);
       }
       // The stage before this one is read: its place takes the step after next.
       if (WIDE && step > 0) wait_for(step - 1);
       fetch(step + L::kAhead);
+      if (step % L::kFlush == L::kFlush - 1 || step == steps - 1) {
+        wait_for(step);
+        tc::fence_after_sync();
+#pragma unroll
+        for (int j = 0; j < L::kSums; ++j) {
+          if (j > step % L::kFlush) break;
+#pragma unroll
+          for (int c = 0; c < kTall / 16; ++c) {
+            float d[16];
+            tc::tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + j * kTall + 16 * c, d);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) total[16 * c + r] += d[r];
+          }
+        }
+        tc::fence_before_sync();
+      }
     }
-    if (!WIDE && steps > 1) wait_for(steps - 2);
-    if (steps > 0) wait_for(steps - 1);
-    tc::fence_after_sync();
     copies_wait<0>();
     __syncthreads();  // the stages are read by all: the sums go over them
     float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int c = 0; c < kTall / 16; ++c) {
-      float v[16] = {};
-#pragma unroll
-      for (int j = 0; j < L::kSums; ++j) {
-        if (j >= steps) break;
-        float d[16];
-        tc::tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + j * kTall + 16 * c, d);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) v[r] += d[r];
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r) sums[(16 * c + r) * L::kSumStride + tid] = v[r];
-    }
+    for (int r = 0; r < kTall; ++r) sums[r * L::kSumStride + tid] = total[r];
     store_sums<BF16, L::kSlots>(p, sums, L::kSumStride, first, count, rank, group * L::kSlots,
                                 p.ad.scales ? __ldcg(p.ad.scales + a) : 1.f);
   }
