@@ -967,6 +967,34 @@ def profile_case(name: str):
         rec_e = torch.empty((2048, fe["rec_pitch"]), dtype=torch.int32, device="cuda")
         for _ in range(2):
             sl.encode(fe, We, rec_e)
+    elif name in ("adapters", "adapters-prefill"):
+        # Low-rank adapters on the 70B layer's fused gate+up: 64 rows with an
+        # adapter each, or 1024 rows of eight adapters, rank 64, three calls.
+        M, n = (64, 64) if name == "adapters" else (1024, 8)
+        A = [torch.randn((n, 64, 8192), device="cuda").bfloat16() * 8192 ** -0.5 for _ in range(2)]
+        B = [torch.randn((n, 28672, 64), device="cuda").bfloat16() * 0.1 for _ in range(2)]
+        ad = sl.Adapters(A, B)
+        ids = torch.arange(M, dtype=torch.int32, device="cuda") % n
+        plan = sl.adapter_plan(ids, n)
+        X = torch.randn((M, 8192), device="cuda").bfloat16()
+        Y = torch.zeros((M, 57344), device="cuda")
+        ws = sl.adapter_workspace(ad, M)
+        for _ in range(3):
+            sl.adapter_apply(ad, plan, X, Y, workspace=ws)
+    elif name == "norm":
+        # Residual sum and both norms of 4096 rows of 8192, three calls.
+        w = torch.ones(8192, dtype=torch.bfloat16, device="cuda")
+        nm = sl.BlockNorm(8192, w_post=w, w_pre=w)
+        y = torch.randn((4096, 8192), device="cuda")
+        h = torch.randn((4096, 8192), device="cuda").bfloat16()
+        x, h_out = torch.empty_like(h), torch.empty_like(h)
+        for _ in range(3):
+            sl.block_norm(nm, y, h, h_out=h_out, x=x)
+    elif name == "glu":
+        GU = torch.randn((2048, 2 * 14336), device="cuda")
+        X = torch.empty((2048, 14336), dtype=torch.bfloat16, device="cuda")
+        for _ in range(3):
+            sl.glu(GU, X)
     elif name == "dense":
         W = torch.randn((57344, 8192), device="cuda").half()
         x = torch.randn(8192, device="cuda").half()
@@ -991,7 +1019,8 @@ def main():
     ap.add_argument("--cpu-seconds", type=float, default=12.0)
     ap.add_argument("--ref-step-seconds", type=float, default=1.0)
     ap.add_argument("--case", choices=("gemv", "gemv3", "gemv-cycle", "decompress", "gemm64", "gemm3x2",
-                                       "gemm16", "dense", "encode"),
+                                       "gemm16", "dense", "encode", "adapters", "adapters-prefill",
+                                       "norm", "glu"),
                     help="run one small single-kernel workload (for ncu) and exit")
     args = ap.parse_args()
     if args.case:

@@ -8,6 +8,7 @@
 #include <set>
 #include <utility>
 
+#include "between_internal.h"
 #include "seedlm_internal.h"
 
 namespace seedlm {

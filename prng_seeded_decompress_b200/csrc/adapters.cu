@@ -9,7 +9,7 @@
 
 #include "launch.cuh"
 #include "seedlm_device.cuh"
-#include "seedlm_internal.h"
+#include "between_internal.h"
 #include "tcgen05.cuh"
 
 namespace seedlm {

@@ -7,7 +7,7 @@
 
 #include <utility>
 
-#include "seedlm_internal.h"
+#include "between_internal.h"
 
 namespace seedlm {
 
