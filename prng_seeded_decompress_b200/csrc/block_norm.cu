@@ -407,16 +407,20 @@ block_norm_stream_kernel(const __grid_constant__ NormArgs p, int M) {
 }
 
 // Many rows that are not aligned for groups of four: each row comes into shared
-// memory as the 16-byte words it lies across, and every thread takes elements a
-// CTA's width apart from there, E of them.  The copies of the next row go out as
-// soon as all threads have taken this one (the barrier inside a sum tells).
+// memory as the 16-byte words it lies across, and every thread takes E elements a
+// CTA's width apart from there.  The copies of the next row go out as soon as all
+// threads have taken this one (the barrier inside a sum tells).  The CTA is as
+// wide as leaves only a thread's last element to be checked against the row's
+// end: threads * (E - 1) < cols <= threads * E.
+constexpr int kRaggedThreads = 512;
+
 template <bool H32, int E>
-__global__ void __launch_bounds__(kStreamThreads, 2)
+__global__ void __launch_bounds__(E >= 16 ? 256 : kRaggedThreads, E >= 16 ? 2 : 1)
 block_norm_ragged_kernel(const __grid_constant__ NormArgs p, int M) {
   extern __shared__ __align__(16) unsigned char shared[];
   float(*red)[4][32] = reinterpret_cast<float(*)[4][32]>(shared);  // [2]: sums of this row and the next
   const seedlm_norm& nm = p.nm;
-  const int cols = nm.cols, tid = threadIdx.x;
+  const int cols = nm.cols, tid = threadIdx.x, threads = blockDim.x;
   constexpr int HB = H32 ? 4 : 2;
   const bool pre = p.x && nm.pre, post = p.y && nm.post, gates = p.y && p.gate;
   const bool gate_row = gates && p.ldg != 0 && nm.dtype != SEEDLM_F32;  // others are read when used
@@ -433,7 +437,7 @@ block_norm_ragged_kernel(const __grid_constant__ NormArgs p, int M) {
     const unsigned char* row = first + m * ld * size;
     const int lead = (int)(reinterpret_cast<uintptr_t>(row) & 15), words = (lead + cols * size + 15) / 16;
     const unsigned char* from = row - lead;
-    for (int c = tid; c < words; c += kStreamThreads) {
+    for (int c = tid; c < words; c += threads) {
       if (from + 16 * c >= first && from + 16 * c + 16 <= end) {
         copy_async<16>(image + 16 * c, from + 16 * c);
       } else {  // a word that leaves the matrix: what of it is in the row
@@ -455,7 +459,9 @@ block_norm_ragged_kernel(const __grid_constant__ NormArgs p, int M) {
     if (gate_row && m < M) fetch(g_image, p.gate, p.ldg, 2, m);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto index = [&](int e) { return tid + kStreamThreads * e; };
+  auto index = [&](int e) { return tid + threads * e; };
+  auto in = [&](int e) { return e < E - 1 || index(e) < cols; };
+  auto clamped = [&](int e) { return e < E - 1 ? index(e) : min(index(e), cols - 1); };
   const float inv = 1.f / cols;
   // As normalise(), over this mapping; `taken` runs after the first barrier.
   auto normalised = [&](float (&v)[E], float* sums, auto taken) {
@@ -468,7 +474,7 @@ block_norm_ragged_kernel(const __grid_constant__ NormArgs p, int M) {
       taken();
       told = true;
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = index(e) < cols ? v[e] - mean : 0.f;
+      for (int e = 0; e < E; ++e) v[e] = in(e) ? v[e] - mean : 0.f;
     }
     float s = 0.f;
 #pragma unroll
@@ -484,13 +490,13 @@ block_norm_ragged_kernel(const __grid_constant__ NormArgs p, int M) {
     if (dtype == SEEDLM_F32) {
       float t[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) t[e] = static_cast<const float*>(a)[min(index(e), cols - 1)];
+      for (int e = 0; e < E; ++e) t[e] = static_cast<const float*>(a)[clamped(e)];
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] = f(v[e], t[e]);
     } else {
       uint16_t t[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) t[e] = static_cast<const uint16_t*>(a)[min(index(e), cols - 1)];
+      for (int e = 0; e < E; ++e) t[e] = static_cast<const uint16_t*>(a)[clamped(e)];
       if (dtype == SEEDLM_BF16) {
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = f(v[e], __uint_as_float((uint32_t)t[e] << 16));
@@ -508,21 +514,21 @@ block_norm_ragged_kernel(const __grid_constant__ NormArgs p, int M) {
   auto cut = [&](float (&v)[E]) {
 #pragma unroll
     for (int e = 0; e < E; ++e)
-      if (index(e) >= cols) v[e] = 0.f;
+      if (!in(e)) v[e] = 0.f;
   };
   auto put = [&](void* to, int64_t row, int dtype, const float (&v)[E]) {
     if (dtype == SEEDLM_F32) {
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (index(e) < cols) static_cast<float*>(to)[row + index(e)] = v[e];
+        if (in(e)) static_cast<float*>(to)[row + index(e)] = v[e];
     } else if (dtype == SEEDLM_BF16) {
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (index(e) < cols) static_cast<__nv_bfloat16*>(to)[row + index(e)] = __float2bfloat16_rn(v[e]);
+        if (in(e)) static_cast<__nv_bfloat16*>(to)[row + index(e)] = __float2bfloat16_rn(v[e]);
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (index(e) < cols) static_cast<__half*>(to)[row + index(e)] = __float2half_rn(v[e]);
+        if (in(e)) static_cast<__half*>(to)[row + index(e)] = __float2half_rn(v[e]);
     }
   };
   grid_launch_dependents();
@@ -537,7 +543,7 @@ block_norm_ragged_kernel(const __grid_constant__ NormArgs p, int M) {
     if (p.y) {
       const float* y = reinterpret_cast<const float*>(image_of(y_image, p.y, p.ldy, 4, m));
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = index(e) < cols ? y[index(e)] : 0.f;
+      for (int e = 0; e < E; ++e) v[e] = in(e) ? y[index(e)] : 0.f;
     }
     auto next_y = [&]() { fetch_y(m + gridDim.x); };
     if (post) {
@@ -723,24 +729,35 @@ int launch_stream(const NormArgs& p, int M, cudaStream_t stream, const DeviceInf
 }
 
 template <bool H32, int E>
-int launch_ragged(const NormArgs& p, int M, cudaStream_t stream, const DeviceInfo& dev) {
+int launch_ragged(const NormArgs& p, int M, int threads, cudaStream_t stream, const DeviceInfo& dev) {
   const int cols = p.nm.cols;
   const int smem = kStreamSums + (cols * 4 + 47) / 16 * 16 + (cols * (H32 ? 4 : 2) + 47) / 16 * 16 +
                    (p.y && p.gate && p.ldg != 0 ? (cols * 2 + 47) / 16 * 16 : 0);
   auto kernel = block_norm_ragged_kernel<H32, E>;
   const int rc = allow_max_smem((const void*)kernel, dev);
   if (rc) return rc;
-  const int ctas = std::max(1, std::min(2, 227 * 1024 / (smem + 1024)));
-  return launch_pdl(kernel, std::min(M, ctas * dev.num_sms), kStreamThreads, (size_t)smem, stream, p, M);
+  // As many CTAs as an SM holds at 128 registers a thread.
+  const int ctas = std::max(1, std::min(512 / threads, 227 * 1024 / (smem + 1024)));
+  return launch_pdl(kernel, std::min<int64_t>(M, (int64_t)ctas * dev.num_sms), threads, (size_t)smem, stream, p, M);
 }
 
+// Threads for E elements each (see above); 0: there is no such width.
+int ragged_threads(int cols, int E, int most) {
+  const int threads = ((cols + E - 1) / E + 31) / 32 * 32;
+  return threads * (E - 1) < cols && threads <= most ? threads : 0;
+}
+
+// SEEDLM_EUNSUPPORTED: no width suits these rows.
 template <bool H32>
 int launch_ragged_of(const NormArgs& p, int M, cudaStream_t stream, const DeviceInfo& dev) {
-  const int each = (p.nm.cols + kStreamThreads - 1) / kStreamThreads;
-  return each <= 4    ? launch_ragged<H32, 4>(p, M, stream, dev)
-         : each <= 12 ? launch_ragged<H32, 12>(p, M, stream, dev)
-         : each <= 20 ? launch_ragged<H32, 20>(p, M, stream, dev)
-                      : launch_ragged<H32, 32>(p, M, stream, dev);
+  const int cols = p.nm.cols;
+  if (const int t = ragged_threads(cols, 32, 256)) return launch_ragged<H32, 32>(p, M, t, stream, dev);
+  if (const int t = ragged_threads(cols, 24, 256)) return launch_ragged<H32, 24>(p, M, t, stream, dev);
+  if (const int t = ragged_threads(cols, 16, 256)) return launch_ragged<H32, 16>(p, M, t, stream, dev);
+  if (const int t = ragged_threads(cols, 12, 512)) return launch_ragged<H32, 12>(p, M, t, stream, dev);
+  if (const int t = ragged_threads(cols, 8, 512)) return launch_ragged<H32, 8>(p, M, t, stream, dev);
+  if (const int t = ragged_threads(cols, 4, 512)) return launch_ragged<H32, 4>(p, M, t, stream, dev);
+  return SEEDLM_EUNSUPPORTED;
 }
 
 template <int ACT>
@@ -770,16 +787,19 @@ int launch_block_norm(const seedlm_norm& nm, int M, const float* y, int64_t ldy,
   // fewer threads with more of a row each, and the next row on its way.
   if (M > 2 * dev.num_sms && groups <= kStreamGroups * kStreamThreads) {
     const bool h32 = (h || h_out) && h_dtype == SEEDLM_F32;
-    if (!vec) return h32 ? launch_ragged_of<true>(p, M, stream, dev) : launch_ragged_of<false>(p, M, stream, dev);
+    if (!vec) {
+      const int rc = h32 ? launch_ragged_of<true>(p, M, stream, dev) : launch_ragged_of<false>(p, M, stream, dev);
+      if (rc != SEEDLM_EUNSUPPORTED) return rc;
+    }
     // The one 16-bit type of the call, if it has one.
     int t16 = x ? x_dtype : SEEDLM_F32;
     for (int t : {h || h_out ? h_dtype : SEEDLM_F32, nm.dtype})
       if (t != SEEDLM_F32) t16 = t16 == SEEDLM_F32 || t16 == t ? t : 3;
-    if (t16 == SEEDLM_F16)
+    if (vec && t16 == SEEDLM_F16)
       return h32 ? launch_stream<true, 0>(p, M, stream, dev) : launch_stream<false, 0>(p, M, stream, dev);
-    if (t16 == SEEDLM_BF16)
+    if (vec && t16 == SEEDLM_BF16)
       return h32 ? launch_stream<true, 1>(p, M, stream, dev) : launch_stream<false, 1>(p, M, stream, dev);
-    return h32 ? launch_stream<true, 2>(p, M, stream, dev) : launch_stream<false, 2>(p, M, stream, dev);
+    if (vec) return h32 ? launch_stream<true, 2>(p, M, stream, dev) : launch_stream<false, 2>(p, M, stream, dev);
   }
   int nv = 1;
   while (groups > nv * kRowThreads) nv *= 2;

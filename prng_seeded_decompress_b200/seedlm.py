@@ -367,62 +367,72 @@ def row_bytes(fmt) -> tuple[int, int]:
 
 # ---------------------------------------------- what runs between the products
 
+# A small call costs little more than its launch, so the checks below are few
+# steps each: torch's types, device and stream are looked up through these.
 _CODES: dict = {}  # torch element types by their code in the library
+_raw_stream = _current_device = None
+
+
+def _bind_torch():
+    global _raw_stream, _current_device
+    import torch
+    _CODES.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
+    _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() makes an object
+    _current_device = torch._C._cuda_getDevice
 
 
 def _any_dtype(t) -> int:
     if not _CODES:
-        import torch
-        _CODES.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
+        _bind_torch()
     code = _CODES.get(t.dtype)
     if code is None:
         raise TypeError(f"expected float16, bfloat16 or float32, got {t.dtype}")
     return code
 
 
-def _f32_ld(t, M: int, cols: int, name: str) -> int:
+def _rows_ld(t, shape: tuple, name: str) -> int:
+    """Leading dimension of a matrix argument of this shape with unit column stride."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {shape[0]} x {shape[1]}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return shape[1]
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return ld if shape[0] > 1 else max(ld, shape[1])
+
+
+def _f32_ld(t, shape: tuple, name: str) -> int:
     if _any_dtype(t) != F32:
         raise TypeError(f"{name} must be float32, got {t.dtype}")
-    return _rows_ld(t, M, cols, name)
-
-
-def _rows_ld(t, M: int, cols: int, name: str) -> int:
-    """Leading dimension of an M x cols argument with unit column stride."""
-    if t.shape != (M, cols):
-        raise ValueError(f"{name} must be {M} x {cols}, got {tuple(t.shape)}")
-    ld, step = t.stride()
-    if step != 1 and cols > 1:
-        raise ValueError(f"{name} must have unit column stride")
-    return ld if M > 1 else max(ld, cols)
+    return _rows_ld(t, shape, name)
 
 
 def _place(tensors) -> int:
-    """The CUDA device that all of `tensors` (some may be None) are on."""
-    device = None
+    """The CUDA device that all of `tensors` are on."""
+    device = tensors[0].get_device()
     for t in tensors:
-        if t is not None:
-            at = t.get_device()
-            if device is None:
-                device = at
-            elif at != device:
-                raise ValueError("tensors must all be on the same CUDA device")
-    if device is None or device < 0:
+        if t.get_device() != device:
+            raise ValueError("tensors must all be on the same CUDA device")
+    if device < 0:
         raise ValueError("tensors must be on a CUDA device")
     return device
 
 
-def _run_on(device: int, stream, fn: str, *args):
-    """The library's `fn` on its arguments and the stream, with `device` current."""
-    import torch
+def _run_on(device: int, stream, fn: str, call, *args):
+    """The library's `call` on its arguments and the stream, with `device` current."""
+    if _raw_stream is None:
+        _bind_torch()
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device)  # current_stream() makes an object
+        stream = _raw_stream(device)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if device == torch.cuda.current_device():
-        rc = getattr(lib, fn)(*args, stream)
+    if device == _current_device():
+        rc = call(*args, stream)
     else:
+        import torch
         with torch.cuda.device(device):
-            rc = getattr(lib, fn)(*args, stream)
+            rc = call(*args, stream)
     if rc != 0:
         _check(fn, rc)
 
@@ -508,8 +518,8 @@ def adapter_plan(ids, n: int, plan: AdapterPlan | None = None, stream=None) -> A
         plan = AdapterPlan(M, n, device=ids.device)
     elif plan.M != M or plan.n != n:
         raise ValueError(f"the plan is for {plan.M} rows and {plan.n} adapters, not {M} and {n}")
-    _run_on(_place((ids, plan.buffer)), stream, "seedlm_adapters_plan", M, plan.n, ids.data_ptr(),
-            plan.buffer.data_ptr())
+    _run_on(_place((ids, plan.buffer)), stream, "seedlm_adapters_plan", lib.seedlm_adapters_plan,
+            M, plan.n, ids.data_ptr(), plan.buffer.data_ptr())
     return plan
 
 
@@ -541,16 +551,20 @@ def adapter_apply(adapters: Adapters, plan: AdapterPlan, X, Y, base=None, worksp
         raise TypeError(f"X must be {adapters.dtype} as the adapters are, got {X.dtype}")
     if plan.n != adapters.n:
         raise ValueError(f"the plan is for {plan.n} adapters, not {adapters.n}")
-    ldx = _rows_ld(X, M, adapters.cols, "X")
-    ldy = _f32_ld(Y, M, adapters.total_rows, "Y")
-    ldb = ldy if base is None else _f32_ld(base, M, adapters.total_rows, "base")
+    out = (M, adapters.total_rows)
+    ldx = _rows_ld(X, (M, adapters.cols), "X")
+    ldy = _f32_ld(Y, out, "Y")
     if workspace is None:
         workspace = adapter_workspace(adapters, M)
-    device = _place((X, Y, base, plan.buffer, workspace))
+    if base is None:
+        ldb, pb, device = ldy, None, _place((X, Y, plan.buffer, workspace))
+    else:
+        ldb, pb = _f32_ld(base, out, "base"), base.data_ptr()
+        device = _place((X, Y, base, plan.buffer, workspace))
     if device != adapters.device:
         raise ValueError("tensors must all be on the same CUDA device")
-    _run_on(device, stream, "seedlm_adapters_apply", adapters.ref, plan.buffer.data_ptr(), M,
-            X.data_ptr(), ldx, None if base is None else base.data_ptr(), ldb, Y.data_ptr(), ldy,
+    _run_on(device, stream, "seedlm_adapters_apply", lib.seedlm_adapters_apply, adapters.ref,
+            plan.buffer.data_ptr(), M, X.data_ptr(), ldx, pb, ldb, Y.data_ptr(), ldy,
             workspace.data_ptr(), workspace.nbytes)
 
 
@@ -577,7 +591,9 @@ class BlockNorm:
             _dense(t, "a weight or bias")
         self.cols = int(cols)
         self.tensors = given
-        self.device = _place(given) if any(t.get_device() >= 0 for t in given) else None
+        self.device = given[0].get_device() if given else -1
+        if any(t.get_device() != self.device for t in given):
+            raise ValueError("tensors must all be on the same CUDA device")
         post = w_post is not None or b_post is not None if post is None else bool(post)
         self.struct = _NormStruct(
             self.cols, 1 if kind == "layer" else 0, _any_dtype(torch.empty(0, dtype=self.dtype)),
@@ -595,36 +611,43 @@ def block_norm(norm: BlockNorm, y, h, h_out=None, x=None, gate=None, stream=None
     like = y if y is not None else h
     if like is None or (h_out is None and x is None):
         raise ValueError("y or h, and h_out or x, must be given")
-    M, cols = like.shape[0] if like.dim() else 0, norm.cols
+    cols = norm.cols
+    shape = (like.shape[0] if like.dim() else 0, cols)
+    tensors = []
     ldy = ldg = ldh = ldo = ldx = ht = xt = 0
     py = pg = ph = po = px = None
     if y is not None:
-        ldy, py = _f32_ld(y, M, cols, "y"), y.data_ptr()
+        ldy, py = _f32_ld(y, shape, "y"), y.data_ptr()
+        tensors.append(y)
     if h is not None:
-        ldh, ph, ht = _rows_ld(h, M, cols, "h"), h.data_ptr(), _any_dtype(h)
+        ldh, ph, ht = _rows_ld(h, shape, "h"), h.data_ptr(), _any_dtype(h)
+        tensors.append(h)
     if h_out is not None:
         if h is not None and h.dtype != h_out.dtype:
             raise TypeError("h and h_out must have one element type")
-        ldo, po, ht = _rows_ld(h_out, M, cols, "h_out"), h_out.data_ptr(), _any_dtype(h_out)
+        ldo, po, ht = _rows_ld(h_out, shape, "h_out"), h_out.data_ptr(), _any_dtype(h_out)
+        tensors.append(h_out)
     if x is not None:
-        ldx, px, xt = _rows_ld(x, M, cols, "x"), x.data_ptr(), _any_dtype(x)
+        ldx, px, xt = _rows_ld(x, shape, "x"), x.data_ptr(), _any_dtype(x)
         if xt == F32:
             raise TypeError("x must be float16 or bfloat16, got float32")
+        tensors.append(x)
     if gate is not None:
         if gate.dtype != norm.dtype:
             raise TypeError(f"gate must be {norm.dtype} as the norm's parameters are")
         if gate.dim() == 1:
             if gate.shape[0] != cols:
-                raise ValueError(f"gate must have {cols} or {M} x {cols} entries")
+                raise ValueError(f"gate must have {cols} or {shape[0]} x {cols} entries")
             _dense(gate, "gate")
         else:
-            ldg = _rows_ld(gate, M, cols, "gate")
+            ldg = _rows_ld(gate, shape, "gate")
         pg = gate.data_ptr()
-    device = _place((y, h, h_out, x, gate))
-    if norm.device is not None and device != norm.device or norm.device is None and norm.tensors:
+        tensors.append(gate)
+    device = _place(tensors)
+    if device != norm.device and norm.tensors:
         raise ValueError("tensors must all be on the same CUDA device")
-    _run_on(device, stream, "seedlm_block_norm", norm.ref, M, py, ldy, pg, ldg, ph, ldh, po, ldo,
-            ht, px, ldx, xt)
+    _run_on(device, stream, "seedlm_block_norm", lib.seedlm_block_norm, norm.ref, shape[0], py, ldy,
+            pg, ldg, ph, ldh, po, ldo, ht, px, ldx, xt)
 
 
 #: Activations of glu().
@@ -639,7 +662,9 @@ def glu(GU, X, act: str = "silu", stream=None):
     if X.dim() != 2:
         raise ValueError("X must be M x cols")
     M, cols = X.shape
-    ldx, xt = _rows_ld(X, M, cols, "X"), _act_dtype(X)
-    ldgu = _f32_ld(GU, M, 2 * cols, "GU")
-    _run_on(_place((X, GU)), stream, "seedlm_glu", M, cols, ACTIVATIONS[act], GU.data_ptr(), ldgu,
-            X.data_ptr(), ldx, xt)
+    ldx, xt = _rows_ld(X, (M, cols), "X"), _any_dtype(X)
+    if xt == F32:
+        raise TypeError("X must be float16 or bfloat16, got float32")
+    ldgu = _f32_ld(GU, (M, 2 * cols), "GU")
+    _run_on(_place((X, GU)), stream, "seedlm_glu", lib.seedlm_glu, M, cols, ACTIVATIONS[act],
+            GU.data_ptr(), ldgu, X.data_ptr(), ldx, xt)
