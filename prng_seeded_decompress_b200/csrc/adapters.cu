@@ -61,7 +61,9 @@ __device__ __forceinline__ void cluster_sync() {
 // warps of a CTA, then over the CTAs through distributed shared memory, then
 // over the bins.  A second walk over the same rows puts each at its place.
 // Latency bound: a few dependent steps, so each lane has 16 of its rows' ids in
-// flight at once and keeps them for the second walk where they are all it has.
+// flight at once and keeps them for the second walk where they are all it has
+// (64 rows: 3.3 us, 16384 rows of 500 adapters: 10.6 us, 38 us with one CTA and
+// the ids read again one by one).
 constexpr int kPlanThreads = 1024, kPlanCtas = 8;
 constexpr int kPlanSteps = 16;  // ids a lane holds
 constexpr int kPlanOneCtaRows = 2048;
@@ -528,7 +530,8 @@ __device__ __forceinline__ void store_sums(const ApplyArgs& p, const float* sums
 // 16 RB ranks of one slice, each of its CTAs one part of the columns and each
 // warp 32 columns of that at a time.  Each warp keeps a ring of its next steps
 // coming into shared memory; a lane copies exactly what it will itself read, so
-// the ring needs no barrier.
+// the ring needs no barrier.  64 rows with adapters of their own, rank 64, two
+// slices of 8192 columns: 135 MB in 32 us (4.3 TB/s).
 template <int RB>
 constexpr int kShrinkLowStages = RB == 4 ? 5 : 6;
 template <int RB, bool WIDE>
@@ -670,7 +673,9 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
 // S for tall tiles (64 rows) on tcgen05.mma: a cluster takes one tile and 128
 // slots of the slices laid end to end (rows of A, the 128-row operand), each of
 // its CTAs one part of the columns, 64 at a time through a ring of shared-memory
-// stages.  Bound by the traffic from L2 (A again for every tile).  The tensor
+// stages.  Bound by the traffic from L2 (A again for every tile) and its latency:
+// 4096 rows, eight adapters of rank 64, two slices of 8192 columns: 200 MB in 33
+// us, 57 with the same products on mma.sync.  The tensor
 // cores cut off what an addition leaves below a sum's last bit, so the stages go
 // to four sums in turn, which after every 32 stages are added up in fp32, rounded.
 // Rows that are not aligned to 16 bytes (not WIDE) come raw, nine words for 64
@@ -885,7 +890,8 @@ __device__ __forceinline__ bool expand_tile(const ApplyArgs& p, int chunks, int 
 // outputs' rows of B and of base coming into shared memory, each lane copying
 // what it will itself read, and takes S straight into registers.  An item of
 // the ring is 32 outputs and a block of up to 64 ranks (32 KC); the last of an
-// output's items brings base.
+// output's items brings base.  64 rows with adapters of their own, rank 64,
+// 57344 outputs: 500 MB in 87 us (5.7 TB/s).
 constexpr int kLowStages = 3;
 template <int KC, bool WIDE>
 constexpr int kLowItemBytes = 2048 * KC * (WIDE ? 1 : 2) + 1024;
@@ -1077,7 +1083,10 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
 // another, and has always asked for the next 16 rows' base before it finishes
 // with these.  B for the next 256 outputs arrives meanwhile: its one place is
 // free as soon as the products are done.  Each CTA goes through its share of all
-// (tile, slice, 256 outputs), in that order, fetching S once for a tile.
+// (tile, slice, 256 outputs), in that order, fetching S once for a tile.  4096
+// rows, eight adapters of rank 64, 57344 outputs: 335 us for 1.94 GB (5.8 TB/s);
+// the products of the same tiles on mma.sync, with the parts of S read from
+// shared memory by every warp, took 500.
 //
 // NB: blocks of 64 ranks; fp16 parts are scaled block by block, so there each
 // block has a sum of its own.

