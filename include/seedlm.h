@@ -319,9 +319,9 @@ SEEDLM_API int64_t seedlm_adapters_plan_words(int32_t M, int32_t n);
  * leading dimensions ldb and ldy.  base == NULL or base == Y (then with
  * ldb == ldy) adds in place, and rows without an adapter are neither read
  * nor written; a base that overlaps Y in another way gives undefined
- * results.  plan: made by seedlm_adapters_plan for this M and ad->n; a plan
- * made for others changes nothing in Y and sets value 4 of
- * seedlm_device_error.  Sums are fp32 in a fixed order per shape; x A^T is
+ * results.  plan: made by seedlm_adapters_plan for this M and ad->n; memory of
+ * that size that holds anything else (a plan of others, zeros) changes nothing
+ * in Y and sets value 4 of seedlm_device_error.  Sums are fp32 in a fixed order per shape; x A^T is
  * kept to 24 bits between the two products.  Any alignment of X, A, B, base
  * and Y that their types allow is accepted; arrays whose rows all begin at
  * multiples of 16 bytes are read fastest.  `workspace`: device memory of at least

@@ -556,7 +556,7 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
   const int row = g < count ? __ldcg(p.plan + first + g) : -1;
   const int r0 = group * R, rank = rank_of(p.ad, a) - r0;  // of this group
   const float scale = p.ad.scales ? __ldcg(p.ad.scales + a) : 1.f;
-  if (rank <= 0) return;
+  if (rank <= 0 || p.ad.rows[s] == 0) return;
   const int k0 = (int)cluster_rank() * p.split_cols, k1 = min(p.ad.cols, k0 + p.split_cols);
   const int blocks = min(RB, (rank + 15) / 16);
 
@@ -742,7 +742,7 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
       src[i] = nullptr;
       if (row < L::kSlots) {
         const int place_of = group * L::kSlots + row, s = place_of / p.slots, r = place_of - s * p.slots;
-        if (s < p.ad.slices && r < rank)
+        if (s < p.ad.slices && r < rank && p.ad.rows[s] > 0)
           src[i] = static_cast<const uint16_t*>(p.ad.A[s]) + a * p.ad.a_adapter[s] + r * p.ad.a_row[s];
       } else {
         const int m = row - L::kSlots < count ? __ldcg(p.plan + first + row - L::kSlots) : -1;
@@ -1546,12 +1546,14 @@ int launch_adapters_apply(const seedlm_adapters& ad, const int32_t* plan, int M,
   p.groups = sh.groups;
   int64_t at = 0;
   for (int s = 0; s < ad.slices; ++s) {
-    p.grain_a[s] = grain_of(ad.A[s], 2 * ad.a_adapter[s], 2 * ad.a_row[s]);
-    p.grain_b[s] = grain_of(ad.B[s], 2 * ad.b_adapter[s], 2 * ad.b_row[s]);
-    p.grain_y[s] = std::min(grain_of(base + at, 4 * ldb, 0), grain_of(Y + at, 4 * ldy, 0));
+    // (A stride that no row is reached by does not count.)
+    const int64_t n1 = ad.n > 1, r1 = ad.rank > 1, j1 = ad.rows[s] > 1, m1 = M > 1;
+    p.grain_a[s] = ad.rows[s] ? grain_of(ad.A[s], n1 * 2 * ad.a_adapter[s], r1 * 2 * ad.a_row[s]) : 16;
+    p.grain_b[s] = grain_of(ad.B[s], n1 * 2 * ad.b_adapter[s], j1 * 2 * ad.b_row[s]);
+    p.grain_y[s] = std::min(grain_of(base + at, m1 * 4 * ldb, 0), grain_of(Y + at, m1 * 4 * ldy, 0));
     at += ad.rows[s];
   }
-  p.grain_x = grain_of(X, 2 * ldx, 0);
+  p.grain_x = grain_of(X, M > 1 ? 2 * ldx : 0, 0);
   const int64_t tiles = sh.tiles;
   p.head = reinterpret_cast<const int4*>(plan + plan_tail(M, ad.n)) + (sh.low ? 0 : 1);
   p.tiles = reinterpret_cast<const int4*>(plan + plan_tail(M, ad.n)) + 2 + (sh.low ? 0 : max_tiles(M, ad.n, kLowRows));

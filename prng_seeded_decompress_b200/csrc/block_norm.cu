@@ -783,9 +783,10 @@ int launch_block_norm(const seedlm_norm& nm, int M, const float* y, int64_t ldy,
   NormArgs p{nm, M, y, ldy, gate, ldg, h, ldh, h_out, ldho, h_dtype, x, ldx, x_dtype};
   const int cols = nm.cols, groups = (cols + 3) / 4;
   if (groups > 4 * kRowThreads) return launch_pdl(block_norm_wide_kernel, M, kWideThreads, 0, stream, p);
-  const bool vec = cols % 4 == 0 && rows_of_four(y, ldy, SEEDLM_F32) && rows_of_four(gate, ldg, nm.dtype) &&
-                   rows_of_four(h, ldh, h_dtype) && rows_of_four(h_out, ldho, h_dtype) &&
-                   rows_of_four(x, ldx, x_dtype) && rows_of_four(nm.w_post, 0, nm.dtype) &&
+  const int64_t m1 = M > 1;  // the leading dimension of one row does not count
+  const bool vec = cols % 4 == 0 && rows_of_four(y, m1 * ldy, SEEDLM_F32) && rows_of_four(gate, m1 * ldg, nm.dtype) &&
+                   rows_of_four(h, m1 * ldh, h_dtype) && rows_of_four(h_out, m1 * ldho, h_dtype) &&
+                   rows_of_four(x, m1 * ldx, x_dtype) && rows_of_four(nm.w_post, 0, nm.dtype) &&
                    rows_of_four(nm.b_post, 0, nm.dtype) && rows_of_four(nm.w_pre, 0, nm.dtype) &&
                    rows_of_four(nm.b_pre, 0, nm.dtype);
   // Few rows: as many threads as there are, for the latency of one row.  Many:

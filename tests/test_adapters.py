@@ -361,6 +361,17 @@ def test_rows_without_an_adapter_are_left_alone(gpu, M, cols, rows):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,cols,outs", [(20, 64, 32), (2048, 1024, 3000)])
+def test_a_slice_without_outputs_is_not_looked_at(gpu, M, cols, outs):
+    d = make(M, cols, [outs, 0, 17], 4, 8, "bf16", "whole", 12)
+    ad = gpu.Adapters(d["A"], d["B"], ranks=d["ranks"], scales=d["scales"])
+    ad.struct.A[1] = ad.struct.B[1] = None
+    Y = torch.empty(M, outs + 17, device="cuda")
+    gpu.adapter_apply(ad, gpu.adapter_plan(d["ids"], 4), d["X"], Y, base=d["base"])
+    assert torch.equal(Y.cpu().double(), reference(d)[0])
+
+
+@pytest.mark.gpu
 def test_without_ranks_and_scales(gpu):
     d = make(20, 64, [32], 4, 8, "f16", "whole", 3, ranks="full")
     d["scales"] = torch.ones(4, device="cuda")

@@ -224,7 +224,7 @@ NORMS = [
     dict(kind="rms", post=True, gate="rows", eps=1e-6, dtype="f16", h="bf16", bias=True, weights=False, y_scale=-1.5),
 ]
 SIZES = [(1, 1), (1, 8192), (3, 7), (2, 64), (5, 129), (4, 1000), (7, 4096), (3, 5001), (2, 8191), (3, 16384), (2, 28672),
-         (1, 32769), (2, 100003), (300, 512), (700, 1001), (2000, 24)]
+         (1, 32769), (2, 100003), (300, 512), (700, 1001), (2000, 24), (400, 8192), (310, 387), (320, 3333), (300, 8191)]
 
 
 @pytest.mark.gpu
@@ -236,7 +236,7 @@ def test_norms_within_the_bound(gpu, which, M, cols, pad, off):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M,cols", [(1, 8192), (3, 5001), (2, 100003), (300, 512)])
+@pytest.mark.parametrize("M,cols", [(1, 8192), (3, 5001), (2, 100003), (300, 512), (700, 1001), (400, 8191)])
 def test_norm_parts_left_out(gpu, M, cols):
     base = dict(NORMS[0], M=M, cols=cols)
     check_norm(gpu, dict(base, y=False))                    # the first block's norm
