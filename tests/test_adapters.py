@@ -406,6 +406,26 @@ def test_shared_and_strided_adapters(gpu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,cols,outs", [(3, 264, 136), (2048, 1024, 2048)])
+def test_offsets_beyond_32_bits(gpu, M, cols, outs):
+    # Adapters 2^31 elements apart; for a few rows also outputs 2^30 floats apart.
+    n, rank, far = 2, 16, 1 << 31
+    d = make(M, cols, [outs], n, rank, "bf16", "whole", 77, ranks="full")
+    for k, shape in (("A", (n, rank, cols)), ("B", (n, outs, rank))):
+        big = torch.empty(far + shape[1] * shape[2], dtype=torch.bfloat16, device="cuda")
+        v = big.as_strided(shape, (far, shape[2], 1))
+        v.copy_(d[k][0])
+        d[k] = [v]
+    ref, _ = reference(d)
+    Y = torch.empty(M, outs, device="cuda")
+    if M == 3:
+        ld = (1 << 30) + 4
+        Y = torch.empty(2 * ld + outs, device="cuda").as_strided((M, outs), (ld, 1))
+    apply(gpu, d, Y, base=d["base"])
+    assert torch.equal(Y.cpu().double(), ref)
+
+
+@pytest.mark.gpu
 def test_a_plan_of_another_batch_changes_nothing_and_says_so(gpu):
     d = make(20, 64, [32], 4, 8, "f16", "whole", 3)
     plan = gpu.adapter_plan(d["ids"], 4)

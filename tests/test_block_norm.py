@@ -253,6 +253,22 @@ def test_norm_parts_left_out(gpu, M, cols):
 
 
 @pytest.mark.gpu
+def test_offsets_beyond_32_bits(gpu):
+    ld, cols = (1 << 30) + 4, 600
+    far = torch.empty(2 * ld + 2 * cols, device="cuda").as_strided((3, 2 * cols), (ld, 1))
+    near = torch.randn(3, 2 * cols, device="cuda")
+    far.copy_(near)
+    nm = gpu.BlockNorm(cols, kind="layer")
+    x, x_far = (torch.empty(3, cols, dtype=torch.float16, device="cuda") for _ in range(2))
+    gpu.block_norm(nm, near[:, :cols], None, x=x)
+    gpu.block_norm(nm, far[:, :cols], None, x=x_far)
+    assert torch.equal(x, x_far)
+    gpu.glu(near, x)
+    gpu.glu(far, x_far)
+    assert torch.equal(x, x_far)
+
+
+@pytest.mark.gpu
 def test_norm_of_constant_huge_and_special_rows(gpu):
     cols = 512
     nm = gpu.BlockNorm(cols, kind="layer", eps=1e-5)
