@@ -281,7 +281,8 @@ SEEDLM_API uint32_t seedlm_lfsr_taps(int32_t K);
  * A[s] + a * a_adapter[s], row r at + r * a_row[s]; B_{s,a} is rows[s] x rank
  * at B[s] + a * b_adapter[s], row j at + j * b_row[s].  Adapter a uses the
  * first ranks[a] rows of A and columns of B (clamped to 0..rank; what lies
- * beyond has no effect); ranks == NULL: all use `rank`.  scales == NULL: 1. */
+ * beyond has no effect); ranks == NULL: all use `rank`.  scales == NULL: 1.
+ * What lies between the rows of X, A and B may be read and has no effect. */
 enum { SEEDLM_MAX_SLICES = 4, SEEDLM_MAX_RANK = 256, SEEDLM_MAX_ADAPTERS = 1024 };
 
 typedef struct seedlm_adapters {

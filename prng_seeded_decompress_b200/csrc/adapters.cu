@@ -349,15 +349,21 @@ __device__ __forceinline__ void copy_small(void* to, const void* from, int bytes
                : "memory");
 }
 
-// Eight elements of a row on their way to a 16-byte unit of shared memory: the
-// first `have` are wanted (0..8), the others become zeros.  before, after: how
-// many elements there are to read before `from` and from it on, in the matrix.
-struct Unit {
-  unsigned char* to;
-  const uint16_t* from;
-  int have;
-  int64_t before, after;
+// A matrix's elements, from the first to behind the last: what lies between two
+// of its rows may be read (and is not used).
+struct Extent {
+  const uint16_t* first;
+  int64_t size;
 };
+__device__ __forceinline__ Extent extent_x(const ApplyArgs& p) { return {p.X, (p.M - 1) * p.ldx + p.ad.cols}; }
+__device__ __forceinline__ Extent extent_a(const ApplyArgs& p, int s) {
+  return {static_cast<const uint16_t*>(p.ad.A[s]),
+          (p.ad.n - 1) * p.ad.a_adapter[s] + (p.ad.rank - 1) * p.ad.a_row[s] + p.ad.cols};
+}
+__device__ __forceinline__ Extent extent_b(const ApplyArgs& p, int s) {
+  return {static_cast<const uint16_t*>(p.ad.B[s]),
+          (p.ad.n - 1) * p.ad.b_adapter[s] + (p.ad.rows[s] - 1) * p.ad.b_row[s] + p.ad.rank};
+}
 
 __device__ __forceinline__ int off_of(const uint16_t* p) { return (int)(reinterpret_cast<uintptr_t>(p) & 15) / 2; }
 
@@ -378,63 +384,67 @@ __device__ __forceinline__ uint4 shift_unit(const uint4& lo, const uint4& hi, in
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A row that is not aligned to 16 bytes comes as the two 16-byte words that each
-// of its units lies across, to `to` and `to + second`, and is shifted when it is
-// read back (take_raw).  Words that would leave the matrix are put together
-// element by element.
-__device__ __forceinline__ void copy_raw(const Unit& u, int second) {
-  if (u.have <= 0) return;
-  const int off = off_of(u.from);
-  if (u.before >= off && u.after >= 16 - off) {
-    copy16(u.to, u.from - off, 16);
-    copy16(u.to + second, u.from - off + 8, 16);
+// Whether the two 16-byte words that the 8 elements at `from` lie across are in
+// the matrix.
+__device__ __forceinline__ bool words_inside(const Extent& m, const uint16_t* from) {
+  const int64_t at = from - m.first - off_of(from);
+  return at >= 0 && at + 16 <= m.size;
+}
+
+// Eight elements of a row, the first `have` of them wanted, on their way to a
+// 16-byte unit of shared memory.  A row that is not aligned to 16 bytes comes as
+// the two 16-byte words that each of its units lies across, to `to` and `to +
+// second`, and is shifted when it is read back (take_raw).  Where a word would
+// leave the matrix (at its two ends), the elements come one by one.
+__device__ __forceinline__ void copy_raw(const Extent& m, unsigned char* to, const uint16_t* from, int have, int second) {
+  if (have <= 0) return;
+  const int off = off_of(from);
+  if (words_inside(m, from)) {
+    copy16(to, from - off, 16);
+    copy16(to + second, from - off + 8, 16);
   } else {
-#pragma unroll 1
-    for (int i = 0; i < u.have; ++i)
-      *reinterpret_cast<uint16_t*>(u.to + (off + i >= 8 ? second - 16 : 0) + 2 * (off + i)) = __ldg(u.from + i);
+    uint16_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = i < have ? __ldg(from + i) : (uint16_t)0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<uint16_t*>(to + (off + i >= 8 ? second - 16 : 0) + 2 * (off + i)) = e[i];
   }
+}
+
+// The same where both words are known to lie in the matrix.
+__device__ __forceinline__ void copy_raw_inside(unsigned char* to, const uint16_t* from, int second) {
+  const uint16_t* at = from - off_of(from);
+  copy16(to, at, 16);
+  copy16(to + second, at + 8, 16);
 }
 
 __device__ __forceinline__ uint4 take_raw(const unsigned char* at, int second, int off, int have) {
-  return shift_unit(*reinterpret_cast<const uint4*>(at), *reinterpret_cast<const uint4*>(at + second), off, have);
+  const uint4 lo = *reinterpret_cast<const uint4*>(at), hi = *reinterpret_cast<const uint4*>(at + second);
+  if (have >= 8) return shift_unit(lo, hi, off, 8);
+  return shift_unit(lo, hi, off, have);
 }
 
 // The same at once, into registers.
-__device__ __forceinline__ uint4 load_unit(const Unit& u) {
-  const int off = off_of(u.from);
-  if (u.have > 0 && u.before >= off && u.after >= 16 - off) {
-    const uint4* at = reinterpret_cast<const uint4*>(u.from - off);
-    return shift_unit(__ldg(at), __ldg(at + 1), off, u.have);
+__device__ __forceinline__ uint4 load_unit(const Extent& m, const uint16_t* from, int have) {
+  if (have <= 0) return make_uint4(0u, 0u, 0u, 0u);
+  const int off = off_of(from);
+  if (words_inside(m, from)) {
+    const uint4* at = reinterpret_cast<const uint4*>(from - off);
+    return shift_unit(__ldg(at), __ldg(at + 1), off, have);
   }
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll 1
-  for (int i = 0; i < u.have; ++i) {
-    const uint32_t e = (uint32_t)__ldg(u.from + i) << (16 * (i % 2));
-    if (i < 2) w[0] |= e;
-    else if (i < 4) w[1] |= e;
-    else if (i < 6) w[2] |= e;
-    else w[3] |= e;
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  uint16_t e[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e[i] = i < have ? __ldg(from + i) : (uint16_t)0;
+  return make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16,
+                    e[6] | (uint32_t)e[7] << 16);
 }
 
 // In a checked build: `have` elements from `at` on if they lie in the matrix that
 // the call describes, else none and the flag; otherwise `have`.
-__device__ __forceinline__ int checked_x(const ApplyArgs& p, const uint16_t* at, int have) {
-  SEEDLM_CHECK_ONLY(const int64_t i = at - p.X; if (have > 0 && (i < 0 ||
-      !SEEDLM_IN_BOUNDS(g_check_flag, i + have - 1, (p.M - 1) * p.ldx + p.ad.cols))) return 0;)
-  return have;
-}
-__device__ __forceinline__ int checked_a(const ApplyArgs& p, int s, const uint16_t* at, int have) {
-  SEEDLM_CHECK_ONLY(const int64_t i = at - static_cast<const uint16_t*>(p.ad.A[s]); if (have > 0 && (i < 0 ||
-      !SEEDLM_IN_BOUNDS(g_check_flag, i + have - 1, (p.ad.n - 1) * p.ad.a_adapter[s] +
-                                                      (p.ad.rank - 1) * p.ad.a_row[s] + p.ad.cols))) return 0;)
-  return have;
-}
-__device__ __forceinline__ int checked_b(const ApplyArgs& p, int s, const uint16_t* at, int have) {
-  SEEDLM_CHECK_ONLY(const int64_t i = at - static_cast<const uint16_t*>(p.ad.B[s]); if (have > 0 && (i < 0 ||
-      !SEEDLM_IN_BOUNDS(g_check_flag, i + have - 1, (p.ad.n - 1) * p.ad.b_adapter[s] +
-                                                      (p.ad.rows[s] - 1) * p.ad.b_row[s] + p.ad.rank))) return 0;)
+__device__ __forceinline__ int checked(const Extent& m, const uint16_t* at, int have) {
+  SEEDLM_CHECK_ONLY(const int64_t i = at - m.first;
+                    if (have > 0 && (i < 0 || !SEEDLM_IN_BOUNDS(g_check_flag, i + have - 1, m.size))) return 0;)
   return have;
 }
 // Whether outputs at .. at + n - 1 of base or Y lie in it.
@@ -584,19 +594,23 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
 #pragma unroll
             for (int j = 2 * b; j < 2 * b + 2; ++j) {
               const int r = 8 * j + g;
-              copy16(to + j * kUnit, A + (r < rank ? r : 0) * a_row, 2 * checked_a(p, s, A + r * a_row, r < rank ? have : 0));
+              copy16(to + j * kUnit, A + (r < rank ? r : 0) * a_row, 2 * checked(extent_a(p, s), A + r * a_row, r < rank ? have : 0));
             }
           }
-        copy16(to + 2 * RB * kUnit, x, 2 * checked_x(p, x, have_x ? have : 0));
+        copy16(to + 2 * RB * kUnit, x, 2 * checked(extent_x(p), x, have_x ? have : 0));
+      } else if (k >= 8 && k + 16 <= p.ad.cols) {
+#pragma unroll 2
+        for (int j = 0; j < 2 * blocks; ++j)
+          if (checked(extent_a(p, s), A + (8 * j + g) * a_row, 8 * j + g < rank ? 8 : 0))
+            copy_raw_inside(to + j * kUnit, A + (8 * j + g) * a_row, 512);
+        if (checked(extent_x(p), x, have_x ? 8 : 0)) copy_raw_inside(to + 2 * RB * kUnit, x, 512);
       } else {
 #pragma unroll 1
         for (int j = 0; j < 2 * blocks; ++j) {
           const int r = 8 * j + g;
-          copy_raw(Unit{to + j * kUnit, A + r * a_row, checked_a(p, s, A + r * a_row, r < rank ? have : 0), r * a_row + k,
-                        (rank - 1 - r) * a_row + p.ad.cols - k}, 512);
+          copy_raw(extent_a(p, s), to + j * kUnit, A + r * a_row, checked(extent_a(p, s), A + r * a_row, r < rank ? have : 0), 512);
         }
-        copy_raw(Unit{to + 2 * RB * kUnit, x, checked_x(p, x, have_x ? have : 0), row * p.ldx + k,
-                      (p.M - 1 - row) * p.ldx + p.ad.cols - k}, 512);
+        copy_raw(extent_x(p), to + 2 * RB * kUnit, x, checked(extent_x(p), x, have_x ? have : 0), 512);
       }
       A += kLowWarps * kStep;
       x += kLowWarps * kStep;
@@ -682,7 +696,7 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
 // elements, and each thread shifts what it copied into place when it is there.
 template <bool WIDE>
 struct ShrinkTallLayout {
-  static constexpr int kThreads = 128, kStages = WIDE ? 4 : 2, kCols = 64, kSlots = 128, kSums = 4, kFlush = 32;
+  static constexpr int kThreads = WIDE ? 128 : 256, kStages = WIDE ? 4 : 2, kCols = 64, kSlots = 128, kSums = 4, kFlush = 32;
   static constexpr int kStageBytes = (kSlots + kTall) * 128;   // rows of A, then rows of X
   static constexpr int kAhead = 3;                             // stages of copies on their way
   static constexpr int kRawBytes = (kSlots + kTall) * 8 * 32;  // two words for each unit
@@ -696,7 +710,7 @@ struct ShrinkTallLayout {
 constexpr uint64_t kTallWaitLimit = 2000000000ull;
 
 template <bool BF16, bool WIDE>
-__global__ void __launch_bounds__(128, WIDE ? 2 : 1)
+__global__ void __launch_bounds__(ShrinkTallLayout<WIDE>::kThreads, WIDE ? 2 : 1)
 adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
   using L = ShrinkTallLayout<WIDE>;
   static_assert(kTall * L::kSumStride * 4 <= L::kBars, "the sums lie over the stages");
@@ -728,33 +742,36 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
     const int k0 = (int)cluster_rank() * p.split_cols, k1 = min(p.ad.cols, k0 + p.split_cols);
     const int steps = k1 > k0 ? (k1 - k0 + L::kCols - 1) / L::kCols : 0;
 
-    // This thread's rows of every stage: unit `unit` of rows row0, row0 + 16, ...
-    // of A (the first eight) and X (the others).  Rows that are not there are
+    // This thread's rows of every stage: unit `unit` of rows row0, row0 + kApart,
+    // ... of A (the first 128) and X (the others).  Rows that are not there are
     // zeroed once in all stages and not copied.
-    constexpr int kMine = (L::kSlots + kTall) / 16;
+    constexpr int kApart = L::kThreads / 8, kMine = (L::kSlots + kTall) / kApart;
     const int unit = tid % 8, row0 = tid / 8;
     const int place = row0 * 128 + (unit ^ (row0 & 7)) * 16;
+    constexpr int kRaw2 = L::kThreads * 32;  // raw words of one of a thread's rows, all threads
     const uint16_t* src[kMine];
     unsigned there = 0;
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      const int row = row0 + 16 * i;
-      src[i] = nullptr;
+    // The row's first element; null: no such row.
+    auto row_of = [&](int i) -> const uint16_t* {
+      const int row = row0 + kApart * i;
       if (row < L::kSlots) {
         const int place_of = group * L::kSlots + row, s = place_of / p.slots, r = place_of - s * p.slots;
-        if (s < p.ad.slices && r < rank && p.ad.rows[s] > 0)
-          src[i] = static_cast<const uint16_t*>(p.ad.A[s]) + a * p.ad.a_adapter[s] + r * p.ad.a_row[s];
-      } else {
-        const int m = row - L::kSlots < count ? __ldcg(p.plan + first + row - L::kSlots) : -1;
-        if (m >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, m, p.M)) src[i] = p.X + m * p.ldx;
+        if (s >= p.ad.slices || r >= rank || p.ad.rows[s] == 0) return nullptr;
+        return static_cast<const uint16_t*>(p.ad.A[s]) + a * p.ad.a_adapter[s] + r * p.ad.a_row[s];
       }
+      const int m = row - L::kSlots < count ? __ldcg(p.plan + first + row - L::kSlots) : -1;
+      return m >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, m, p.M) ? p.X + m * p.ldx : nullptr;
+    };
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      src[i] = row_of(i);
       there |= (unsigned)(src[i] != nullptr) << i;
       if (!src[i])
         for (int st = 0; st < L::kStages; ++st)
-          *reinterpret_cast<uint4*>(smem + st * L::kStageBytes + i * 2048 + place) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(smem + st * L::kStageBytes + i * kApart * 128 + place) = make_uint4(0u, 0u, 0u, 0u);
     }
-    auto checked = [&](int i, const uint16_t* at, int have) {
-      return 16 * i < L::kSlots ? checked_a(p, (group * L::kSlots + row0 + 16 * i) / p.slots, at, have) : checked_x(p, at, have);
+    auto extent_of = [&](int i) {
+      return kApart * i < L::kSlots ? extent_a(p, (group * L::kSlots + row0 + kApart * i) / p.slots) : extent_x(p);
     };
     auto fetch = [&](int step) {
       if (step < steps) {
@@ -763,12 +780,21 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
           unsigned char* to = smem + step % L::kStages * L::kStageBytes + place;
 #pragma unroll
           for (int i = 0; i < kMine; ++i)
-            if (there >> i & 1) copy16(to + i * 2048, src[i] + k, 2 * checked(i, src[i] + k, have));
+            if (there >> i & 1) copy16(to + i * kApart * 128, src[i] + k, 2 * checked(extent_of(i), src[i] + k, have));
         } else {
           unsigned char* to = smem + L::kRaw + step % L::kAhead * L::kRawBytes + tid * 16;
+          if (k >= 8 && k + 16 <= p.ad.cols) {
 #pragma unroll
-          for (int i = 0; i < kMine; ++i)  // within the row: its neighbours are not always the same matrix's
-            if (there >> i & 1) copy_raw(Unit{to + i * 4096, src[i] + k, checked(i, src[i] + k, have), k, p.ad.cols - k}, 2048);
+            for (int i = 0; i < kMine; ++i)
+              if ((there >> i & 1) && checked(extent_of(i), src[i] + k, 8)) copy_raw_inside(to + i * kRaw2, src[i] + k, kRaw2 / 2);
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < kMine; ++i)
+              if (there >> i & 1) {
+                const uint16_t* from = row_of(i) + k;
+                copy_raw(extent_of(i), to + i * kRaw2, from, checked(extent_of(i), from, have), kRaw2 / 2);
+              }
+          }
         }
       }
       copies_commit();
@@ -790,7 +816,7 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
 #pragma unroll
         for (int i = 0; i < kMine; ++i)
           if (there >> i & 1)
-            *reinterpret_cast<uint4*>(to + i * 2048) = take_raw(raw + i * 4096, 2048, off_of(src[i] + k), have);
+            *reinterpret_cast<uint4*>(to + i * kApart * 128) = take_raw(raw + i * kRaw2, kRaw2 / 2, off_of(src[i]), have);
       }
       tc::fence_proxy_async();
       __syncthreads();
@@ -807,7 +833,7 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
       // The stage before this one is read: its place takes the step after next.
       if (WIDE && step > 0) wait_for(step - 1);
       fetch(step + L::kAhead);
-      if (step % L::kFlush == L::kFlush - 1 || step == steps - 1) {
+      if (tid < L::kSlots && (step % L::kFlush == L::kFlush - 1 || step == steps - 1)) {
         wait_for(step);
         tc::fence_after_sync();
 #pragma unroll
@@ -828,7 +854,8 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
     __syncthreads();  // the stages are read by all: the sums go over them
     float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int r = 0; r < kTall; ++r) sums[r * L::kSumStride + tid] = total[r];
+    for (int r = 0; r < kTall; ++r)
+      if (tid < L::kSlots) sums[r * L::kSumStride + tid] = total[r];
     store_sums<BF16, L::kSlots>(p, sums, L::kSumStride, first, count, rank, group * L::kSlots,
                                 p.ad.scales ? __ldcg(p.ad.scales + a) : 1.f);
   }
@@ -950,15 +977,14 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
         for (int c = 0; c < KC; ++c) {
           unsigned char* to = into + (4 * c + j) * 512;
           const uint16_t* from = b + kStep * c;
-          const int wanted = checked_b(p, x.s, from, whole || n < x.c1 ? have[c] : 0);
+          const int wanted = checked(extent_b(p, x.s), from, whole || n < x.c1 ? have[c] : 0);
           if (WIDE) {
             copy16_short(to, from, 2 * wanted);
           } else if (eights) {
             copy_small<8>(to, from, max(0, min(8, 2 * wanted)));
             copy_small<8>(to + 8, from + 4, max(0, 2 * wanted - 8));
           } else {
-            const int r = fetch_k + kStep * c + 8 * q;
-            copy_raw(Unit{to, from, wanted, n * b_row + r, (p.ad.rows[x.s] - 1 - n) * b_row + x.rank - r}, 2048 * KC);
+            copy_raw(extent_b(p, x.s), to, from, wanted, 2048 * KC);
           }
         }
         b += b_row;
@@ -966,12 +992,18 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
       b_next += 64;
       fetch_k += 64;
       if (!MANY || fetch_k >= x.rank) {  // the last ranks of these outputs
-        if (vec_y && whole) {
+        if (whole) {
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            if (from[e])
-              copy16(into + kItemBytes - 1024 + e * 512, from[e] + fetch_n,
-                     checked_y(p, from[e] + fetch_n, p.base, p.ldb, 4) ? 16 : 0);
+            if (from[e] && checked_y(p, from[e] + fetch_n, p.base, p.ldb, 4)) {
+              unsigned char* to = into + kItemBytes - 1024 + e * 512;
+              if (vec_y) {
+                copy16(to, from[e] + fetch_n, 16);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) copy_small<4>(to + 4 * j, from[e] + fetch_n + j, 4);
+              }
+            }
         }
         b_next += kRound * b_row - 64 * groups;
         fetch_n += kRound;
@@ -1049,15 +1081,22 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
       }
     k += 64;
     if (!MANY || k >= x.rank) {
-      const bool whole = vec_y && n0 + 32 <= x.c1;
+      const bool whole = n0 + 32 <= x.c1;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (!to[e]) continue;
         const float4 d = make_float4(total[0][e], total[0][2 + e], total[1][e], total[1][2 + e]);
         if (whole) {
           const float4 b = *reinterpret_cast<const float4*>(item_at + kItemBytes - 1024 + e * 512);
-          if (checked_y(p, to[e] + n0, p.Y, p.ldy, 4))
+          if (!checked_y(p, to[e] + n0, p.Y, p.ldy, 4)) continue;
+          if (vec_y) {
             *reinterpret_cast<float4*>(to[e] + n0) = make_float4(b.x + d.x, b.y + d.y, b.z + d.z, b.w + d.w);
+          } else {
+            to[e][n0] = b.x + d.x;
+            to[e][n0 + 1] = b.y + d.y;
+            to[e][n0 + 2] = b.z + d.z;
+            to[e][n0 + 3] = b.w + d.w;
+          }
         } else {
           add4_slow(p, to[e] + n0, from[e] + n0, d, x.c1 - n0 - 4 * g);
         }
@@ -1162,41 +1201,53 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
       from_row[tid] = (in ? m * p.ldb : 0) + p.slice_at[s];
       to_row[tid] = (in ? m * p.ldy : 0) + p.slice_at[s];
     }
-    // B of outputs c0 + 256 i + (0 .. 255): output 2 j + h is row j of half h.
+    // B of outputs c0 + 256 i + (0 .. 255): output 2 j + h is row j of half h, or,
+    // where base and Y cannot be read in pairs, output 128 h + j.
+    const int of_row = pairs ? 2 : 1, of_half = pairs ? 1 : 128;
     auto fetch = [&](int i) {
-      const int n = c0 + i * kOut + 2 * row0;
+      const int n = c0 + i * kOut + of_row * row0;
       const uint16_t* src = B + n * b_row + 8 * unit;
+      const int64_t b_rows = 16 * of_row * b_row, b_half = of_half * b_row;
       unsigned char* to = smem + L::kB + place;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const int have = max(0, min(8, rank - 64 * b - 8 * unit));
-        auto unit_of = [&](int u) {
-          const int j = u / 2, h = u % 2, at = n + 32 * j + h;
-          return Unit{to + (h * NB + b) * 128 * 128 + j * 16 * 128, src + 64 * b + (32 * j + h) * b_row,
-                      checked_b(p, s, src + 64 * b + (32 * j + h) * b_row, at < rows ? have : 0), at * b_row + 64 * b + 8 * unit,
-                      (rows - 1 - at) * b_row + rank - 64 * b - 8 * unit};
+        // Unit u: row j of half h, its place and its wanted elements.
+        auto unit_of = [&](int u, unsigned char*& place_of, const uint16_t*& from) {
+          const int j = u / 2, h = u % 2, at = n + 16 * of_row * j + of_half * h;
+          place_of = to + (h * NB + b) * 128 * 128 + j * 16 * 128;
+          from = src + 64 * b + j * b_rows + h * b_half;
+          return checked(extent_b(p, s), from, at < rows ? have : 0);
         };
+        unsigned char* at;
+        const uint16_t* from;
         if (WIDE) {
 #pragma unroll
           for (int u = 0; u < 16; ++u) {
-            const Unit x = unit_of(u);
-            copy16_short(x.to, x.from, 2 * x.have);
+            const int wanted = unit_of(u, at, from);
+            copy16_short(at, from, 2 * wanted);
           }
         } else if (p.grain_b[s] >= 8) {
 #pragma unroll 2
           for (int u = 0; u < 16; ++u) {
-            const Unit x = unit_of(u);
-            copy_small<8>(x.to, x.from, max(0, min(8, 2 * x.have)));
-            copy_small<8>(x.to + 8, x.from + 4, max(0, 2 * x.have - 8));
+            const int wanted = unit_of(u, at, from);
+            copy_small<8>(at, from, max(0, min(8, 2 * wanted)));
+            copy_small<8>(at + 8, from + 4, max(0, 2 * wanted - 8));
           }
         } else {
 #pragma unroll 1
           for (int u0 = 0; u0 < 16; u0 += 4) {
             uint4 v[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = load_unit(unit_of(u0 + u));
+            for (int u = 0; u < 4; ++u) {
+              const int wanted = unit_of(u0 + u, at, from);
+              v[u] = load_unit(extent_b(p, s), from, wanted);
+            }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) *reinterpret_cast<uint4*>(unit_of(u0 + u).to) = v[u];
+            for (int u = 0; u < 4; ++u) {
+              unit_of(u0 + u, at, from);
+              *reinterpret_cast<uint4*>(at) = v[u];
+            }
           }
         }
       }
@@ -1256,20 +1307,28 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
     // adapter's other tiles (measured without: B came from memory every time).
     float2 ahead[kQ];
     auto ask = [&](int i, int q) {
-      const int n = c0 + i * kOut + 2 * tid;
+      const int n = c0 + i * kOut + of_row * tid;
       const float* from = p.base + n;
-      if (pairs && count >= kQ * (q + 1) && c0 + (i + 1) * kOut <= rows) {
+      if (count >= kQ * (q + 1) && c0 + (i + 1) * kOut <= rows) {
+        if (pairs) {
 #pragma unroll
-        for (int r = 0; r < kQ; ++r)
-          if (checked_y(p, from + from_row[kQ * q + r], p.base, p.ldb, 2))
-            ahead[r] = __ldcs(reinterpret_cast<const float2*>(from + from_row[kQ * q + r]));
+          for (int r = 0; r < kQ; ++r)
+            if (checked_y(p, from + from_row[kQ * q + r], p.base, p.ldb, 2))
+              ahead[r] = __ldcs(reinterpret_cast<const float2*>(from + from_row[kQ * q + r]));
+        } else {
+#pragma unroll
+          for (int r = 0; r < kQ; ++r) {
+            const float* at = from + from_row[kQ * q + r];
+            if (checked_y(p, at, p.base, p.ldb, of_half + 1)) ahead[r] = make_float2(__ldcs(at), __ldcs(at + of_half));
+          }
+        }
       } else {
 #pragma unroll
         for (int r = 0; r < kQ; ++r) {
           const float* at = from + from_row[kQ * q + r];
-          const bool in = kQ * q + r < count && (n >= rows || checked_y(p, at, p.base, p.ldb, min(2, rows - n)));
-          ahead[r].x = in && n < rows ? __ldcg(at) : 0.f;
-          ahead[r].y = in && n + 1 < rows ? __ldcg(at + 1) : 0.f;
+          const bool in = kQ * q + r < count;
+          ahead[r].x = in && n < rows && checked_y(p, at, p.base, p.ldb, 1) ? __ldcg(at) : 0.f;
+          ahead[r].y = in && n + of_half < rows && checked_y(p, at + of_half, p.base, p.ldb, 1) ? __ldcg(at + of_half) : 0.f;
         }
       }
     };
@@ -1287,7 +1346,7 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
         tc::fence_after_sync();
         if (i + 1 < items) fetch(i + 1);
       }
-      const int n = c0 + i * kOut + 2 * tid;
+      const int n = c0 + i * kOut + of_row * tid;
       float* to = p.Y + n;
 #pragma unroll
       for (int q = 0; q < T / kQ; ++q) {
@@ -1312,18 +1371,28 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
               }
           }
         if (!ok) continue;
-        if (pairs && count >= kQ * (q + 1) && c0 + (i + 1) * kOut <= rows) {
+        if (count >= kQ * (q + 1) && c0 + (i + 1) * kOut <= rows) {
+          if (pairs) {
 #pragma unroll
-          for (int r = 0; r < kQ; ++r)
-            if (checked_y(p, to + to_row[kQ * q + r], p.Y, p.ldy, 2))
-              __stcs(reinterpret_cast<float2*>(to + to_row[kQ * q + r]), v[r]);
+            for (int r = 0; r < kQ; ++r)
+              if (checked_y(p, to + to_row[kQ * q + r], p.Y, p.ldy, 2))
+                __stcs(reinterpret_cast<float2*>(to + to_row[kQ * q + r]), v[r]);
+          } else {
+#pragma unroll
+            for (int r = 0; r < kQ; ++r) {
+              float* at = to + to_row[kQ * q + r];
+              if (!checked_y(p, at, p.Y, p.ldy, of_half + 1)) continue;
+              __stcs(at, v[r].x);
+              __stcs(at + of_half, v[r].y);
+            }
+          }
         } else {
 #pragma unroll
           for (int r = 0; r < kQ; ++r) {
             float* at = to + to_row[kQ * q + r];
-            const bool in = kQ * q + r < count && (n >= rows || checked_y(p, at, p.Y, p.ldy, min(2, rows - n)));
-            if (in && n < rows) at[0] = v[r].x;
-            if (in && n + 1 < rows) at[1] = v[r].y;
+            const bool in = kQ * q + r < count;
+            if (in && n < rows && checked_y(p, at, p.Y, p.ldy, 1)) at[0] = v[r].x;
+            if (in && n + of_half < rows && checked_y(p, at + of_half, p.Y, p.ldy, 1)) at[of_half] = v[r].y;
           }
         }
       }
@@ -1379,6 +1448,8 @@ struct ShrinkShape {
   int slots, blocks, groups, splits, split_cols;
 };
 
+int slots_of(const seedlm_adapters& ad) { return ad.rank <= 32 ? 32 : (ad.rank + 63) / 64 * 64; }
+
 // Whether a projection takes tiles of 8 rows or of 64.  In units of 57344 outputs
 // and inputs, a low tile was measured at 1.65 us whatever its rows and ranks, a
 // tall one at 3.75 us and 0.03 us a row, and its two kernels at 13 us more for
@@ -1396,7 +1467,7 @@ bool takes_low_tiles(const seedlm_adapters& ad, int M) {
 
 ShrinkShape shrink_shape(const seedlm_adapters& ad, int M, const DeviceInfo& dev) {
   ShrinkShape sh{};
-  sh.slots = ad.rank <= 32 ? 32 : (ad.rank + 63) / 64 * 64;
+  sh.slots = slots_of(ad);
   sh.low = takes_low_tiles(ad, M);
   sh.tiles = max_tiles(M, ad.n, sh.low ? kLowRows : kTall);
   int64_t clusters = sh.tiles, round;
@@ -1466,7 +1537,7 @@ int launch_expand_tall(const ApplyArgs& p, int64_t items, int chunks, cudaStream
                                 dev, p, chunks, (int)(p.base == p.Y));
 }
 
-template <bool BF16, bool WIDE>
+template <bool BF16, bool WIDE, bool WIDE_B>
 int launch_products(ApplyArgs& p, const ShrinkShape& sh, int64_t tiles, cudaStream_t stream, const DeviceInfo& dev) {
   const bool low = sh.low;
   int rc;
@@ -1502,12 +1573,12 @@ int launch_products(ApplyArgs& p, const ShrinkShape& sh, int64_t tiles, cudaStre
   const int64_t grid = chunks * tiles;
   if (grid > INT32_MAX) return SEEDLM_EUNSUPPORTED;
   if (low)
-    return p.slots == 32   ? launch_expand_low<BF16, WIDE, 1, false>(p, grid, (int)chunks, stream, dev)
-           : p.slots == 64 ? launch_expand_low<BF16, WIDE, 2, false>(p, grid, (int)chunks, stream, dev)
-                           : launch_expand_low<BF16, WIDE, 2, true>(p, grid, (int)chunks, stream, dev);
-  return p.blocks == 1   ? launch_expand_tall<BF16, WIDE, 1>(p, grid, (int)chunks, stream, dev)
-         : p.blocks == 2 ? launch_expand_tall<BF16, WIDE, 2>(p, grid, (int)chunks, stream, dev)
-                         : launch_expand_tall<BF16, WIDE, 4>(p, grid, (int)chunks, stream, dev);
+    return p.slots == 32   ? launch_expand_low<BF16, WIDE_B, 1, false>(p, grid, (int)chunks, stream, dev)
+           : p.slots == 64 ? launch_expand_low<BF16, WIDE_B, 2, false>(p, grid, (int)chunks, stream, dev)
+                           : launch_expand_low<BF16, WIDE_B, 2, true>(p, grid, (int)chunks, stream, dev);
+  return p.blocks == 1   ? launch_expand_tall<BF16, WIDE_B, 1>(p, grid, (int)chunks, stream, dev)
+         : p.blocks == 2 ? launch_expand_tall<BF16, WIDE_B, 2>(p, grid, (int)chunks, stream, dev)
+                         : launch_expand_tall<BF16, WIDE_B, 4>(p, grid, (int)chunks, stream, dev);
 }
 
 // Bytes of S, then those of its factors.
@@ -1518,16 +1589,15 @@ int64_t sums_bytes(const seedlm_adapters& ad, int M, int slots) {
 
 }  // namespace
 
-int64_t adapters_workspace_bytes(const seedlm_adapters& ad, int M, const DeviceInfo& dev) {
-  const ShrinkShape sh = shrink_shape(ad, M, dev);
-  const int64_t blocks = std::max(1, sh.slots / 64);
-  return sums_bytes(ad, M, sh.slots) + (ad.dtype == SEEDLM_F16 ? (int64_t)M * ad.slices * blocks * 4 : 0);
+int64_t adapters_workspace_bytes(const seedlm_adapters& ad, int M, const DeviceInfo&) {
+  const int slots = slots_of(ad);
+  const int64_t blocks = std::max(1, slots / 64);
+  return sums_bytes(ad, M, slots) + (ad.dtype == SEEDLM_F16 ? (int64_t)M * ad.slices * blocks * 4 : 0);
 }
 
 int launch_adapters_apply(const seedlm_adapters& ad, const int32_t* plan, int M, const uint16_t* X, int64_t ldx,
                           const float* base, int64_t ldb, float* Y, int64_t ldy, void* workspace, cudaStream_t stream,
                           const DeviceInfo& dev) {
-  const ShrinkShape sh = shrink_shape(ad, M, dev);
   ApplyArgs p{};
   p.ad = ad;
   p.plan = plan;
@@ -1538,12 +1608,6 @@ int launch_adapters_apply(const seedlm_adapters& ad, const int32_t* plan, int M,
   p.ldb = ldb;
   p.Y = Y;
   p.ldy = ldy;
-  p.S = static_cast<uint16_t*>(workspace);
-  p.unscale = reinterpret_cast<float*>(static_cast<char*>(workspace) + sums_bytes(ad, M, sh.slots));
-  p.slots = sh.slots;
-  p.blocks = std::max(1, sh.slots / 64);
-  p.split_cols = sh.split_cols;
-  p.groups = sh.groups;
   int64_t at = 0;
   for (int s = 0; s < ad.slices; ++s) {
     // (A stride that no row is reached by does not count.)
@@ -1554,17 +1618,31 @@ int launch_adapters_apply(const seedlm_adapters& ad, const int32_t* plan, int M,
     at += ad.rows[s];
   }
   p.grain_x = grain_of(X, M > 1 ? 2 * ldx : 0, 0);
+  bool wide = p.grain_x == 16, wide_b = true;
+  for (int s = 0; s < ad.slices; ++s) {
+    wide = wide && p.grain_a[s] == 16;
+    wide_b = wide_b && p.grain_b[s] == 16;
+  }
+  const ShrinkShape sh = shrink_shape(ad, M, dev);
+  p.S = static_cast<uint16_t*>(workspace);
+  p.unscale = reinterpret_cast<float*>(static_cast<char*>(workspace) + sums_bytes(ad, M, sh.slots));
+  p.slots = sh.slots;
+  p.blocks = std::max(1, sh.slots / 64);
+  p.split_cols = sh.split_cols;
+  p.groups = sh.groups;
   const int64_t tiles = sh.tiles;
   p.head = reinterpret_cast<const int4*>(plan + plan_tail(M, ad.n)) + (sh.low ? 0 : 1);
   p.tiles = reinterpret_cast<const int4*>(plan + plan_tail(M, ad.n)) + 2 + (sh.low ? 0 : max_tiles(M, ad.n, kLowRows));
   if (tiles * ad.slices * sh.groups * sh.splits > INT32_MAX) return SEEDLM_EUNSUPPORTED;
-  bool wide = p.grain_x == 16;
-  for (int s = 0; s < ad.slices; ++s) wide = wide && p.grain_a[s] == 16 && p.grain_b[s] == 16;
   if (ad.dtype == SEEDLM_BF16)
-    return wide ? launch_products<true, true>(p, sh, tiles, stream, dev)
-                : launch_products<true, false>(p, sh, tiles, stream, dev);
-  return wide ? launch_products<false, true>(p, sh, tiles, stream, dev)
-              : launch_products<false, false>(p, sh, tiles, stream, dev);
+    return wide     ? wide_b ? launch_products<true, true, true>(p, sh, tiles, stream, dev)
+                             : launch_products<true, true, false>(p, sh, tiles, stream, dev)
+           : wide_b ? launch_products<true, false, true>(p, sh, tiles, stream, dev)
+                    : launch_products<true, false, false>(p, sh, tiles, stream, dev);
+  return wide     ? wide_b ? launch_products<false, true, true>(p, sh, tiles, stream, dev)
+                           : launch_products<false, true, false>(p, sh, tiles, stream, dev)
+         : wide_b ? launch_products<false, false, true>(p, sh, tiles, stream, dev)
+                  : launch_products<false, false, false>(p, sh, tiles, stream, dev);
 }
 
 int read_and_clear_plan_mismatch(unsigned int* out) {
