@@ -336,6 +336,12 @@ __device__ __forceinline__ void copy16_short(void* to, const void* from, int byt
                "l"(from), "r"(bytes)
                : "memory");
 }
+// The same, or nothing.
+__device__ __forceinline__ void copy16_if(bool on, uint32_t to, const void* from, int bytes) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(to),
+               "l"(from), "r"(bytes), "r"((uint32_t)on)
+               : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT>
 __device__ __forceinline__ void copies_wait() {
@@ -696,7 +702,7 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
 // elements, and each thread shifts what it copied into place when it is there.
 template <bool WIDE>
 struct ShrinkTallLayout {
-  static constexpr int kThreads = WIDE ? 128 : 256, kStages = WIDE ? 4 : 2, kCols = 64, kSlots = 128, kSums = 4, kFlush = 32;
+  static constexpr int kThreads = 256, kStages = WIDE ? 4 : 2, kCols = 64, kSlots = 128, kSums = 4, kFlush = 32;
   static constexpr int kStageBytes = (kSlots + kTall) * 128;   // rows of A, then rows of X
   static constexpr int kAhead = 3;                             // stages of copies on their way
   static constexpr int kRawBytes = (kSlots + kTall) * 8 * 32;  // two words for each unit
@@ -773,14 +779,17 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
     auto extent_of = [&](int i) {
       return kApart * i < L::kSlots ? extent_a(p, (group * L::kSlots + row0 + kApart * i) / p.slots) : extent_x(p);
     };
-    auto fetch = [&](int step) {
+    const uint32_t to_stages = tc::smem_u32(smem) + place;
+    auto fetch = [&](int step, int st) {
       if (step < steps) {
         const int k = k0 + step * L::kCols + 8 * unit, have = max(0, min(8, k1 - k));
         if (WIDE) {
-          unsigned char* to = smem + step % L::kStages * L::kStageBytes + place;
 #pragma unroll
-          for (int i = 0; i < kMine; ++i)
-            if (there >> i & 1) copy16(to + i * kApart * 128, src[i] + k, 2 * checked(extent_of(i), src[i] + k, have));
+          for (int i = 0; i < kMine; ++i) {
+            int wanted = have;
+            SEEDLM_CHECK_ONLY(if (there >> i & 1) wanted = checked(extent_of(i), src[i] + k, have);)
+            copy16_if(there & 1u << i, to_stages + st * L::kStageBytes + i * kApart * 128, src[i] + k, 2 * wanted);
+          }
         } else {
           unsigned char* to = smem + L::kRaw + step % L::kAhead * L::kRawBytes + tid * 16;
           if (k >= 8 && k + 16 <= p.ad.cols) {
@@ -799,50 +808,64 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
       }
       copies_commit();
     };
-    for (int i = 0; i < L::kAhead; ++i) fetch(i);
+    for (int i = 0; i < L::kAhead; ++i) fetch(i, i);
     const uint32_t idesc = tc::idesc_f16(kTall, BF16 ? 1 : 0);
     auto wait_for = [&](int step) {
       ok = tc::mbar_wait_or_abort(bars + 8 * (step % L::kStages), (step / L::kStages) & 1, kTallWaitLimit, slot + 1) && ok;
     };
-    float total[kTall] = {};  // of slot tid
-    for (int step = 0; step < steps; ++step) {
-      copies_wait<L::kAhead - 1>();
-      const int st = step % L::kStages;
-      if (!WIDE) {
-        if (step >= L::kStages) wait_for(step - L::kStages);  // the stage is free
-        const int k = k0 + step * L::kCols + 8 * unit, have = max(0, min(8, k1 - k));
-        const unsigned char* raw = smem + L::kRaw + step % L::kAhead * L::kRawBytes + tid * 16;
-        unsigned char* to = smem + st * L::kStageBytes + place;
+    // Of slot tid % 128, rows kHalf (tid / 128) on.
+    constexpr int kHalf = kTall * L::kSlots / L::kThreads;
+    const int row1 = tid / L::kSlots * kHalf;
+    float total[kHalf] = {};
+    // The stages are spelled out, so that a copy is an address and a predicate: with
+    // few warps to a scheduler the instructions of a step are its time (2750 rows,
+    // 14336 columns, four adapters of rank 8, both products: 53.5 us; 62.4 with
+    // 128 threads, a branch to a copy and a loop over the stages).
+    constexpr int kTurns = WIDE ? L::kStages : 1;
+    for (int step0 = 0; step0 < steps; step0 += kTurns) {
 #pragma unroll
-        for (int i = 0; i < kMine; ++i)
-          if (there >> i & 1)
-            *reinterpret_cast<uint4*>(to + i * kApart * 128) = take_raw(raw + i * kRaw2, kRaw2 / 2, off_of(src[i]), have);
-      }
-      tc::fence_proxy_async();
-      __syncthreads();
-      if (warp == 0) {
-        tc::fence_after_sync();
-        const int turn = step % L::kFlush;
-        const uint64_t w = tc::smem_desc_sw128(tc::smem_u32(smem + st * L::kStageBytes));
-        const uint64_t x = w + L::kSlots * 128 / 16;
+      for (int u = 0; u < kTurns; ++u) {
+        const int step = step0 + u;
+        if (step >= steps) break;
+        const int st = WIDE ? u : step % L::kStages;
+        copies_wait<L::kAhead - 1>();
+        if (!WIDE) {
+          if (step >= L::kStages) wait_for(step - L::kStages);  // the stage is free
+          const int k = k0 + step * L::kCols + 8 * unit, have = max(0, min(8, k1 - k));
+          const unsigned char* raw = smem + L::kRaw + step % L::kAhead * L::kRawBytes + tid * 16;
+          unsigned char* to = smem + st * L::kStageBytes + place;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc::mma_f16_ss_warp(tmem + turn % L::kSums * kTall, w + 2 * k, x + 2 * k, idesc, turn >= L::kSums || k > 0);
-        tc::mma_commit_warp(bars + 8 * st);
+          for (int i = 0; i < kMine; ++i)
+            if (there >> i & 1)
+              *reinterpret_cast<uint4*>(to + i * kApart * 128) = take_raw(raw + i * kRaw2, kRaw2 / 2, off_of(src[i]), have);
+        }
+        tc::fence_proxy_async();
+        __syncthreads();
+        if (warp == 0) {
+          tc::fence_after_sync();
+          const int turn = step % L::kFlush;
+          const uint64_t w = tc::smem_desc_sw128(tc::smem_u32(smem + st * L::kStageBytes));
+          const uint64_t x = w + L::kSlots * 128 / 16;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc::mma_f16_ss_warp(tmem + turn % L::kSums * kTall, w + 2 * k, x + 2 * k, idesc, turn >= L::kSums || k > 0);
+          tc::mma_commit_warp(bars + 8 * st);
+        }
+        // The stage before this one is read: its place takes the step after next.
+        if (WIDE && step > 0) wait_for(step - 1);
+        fetch(step + L::kAhead, (u + L::kAhead) % L::kStages);
       }
-      // The stage before this one is read: its place takes the step after next.
-      if (WIDE && step > 0) wait_for(step - 1);
-      fetch(step + L::kAhead);
-      if (tid < L::kSlots && (step % L::kFlush == L::kFlush - 1 || step == steps - 1)) {
-        wait_for(step);
+      const int last = min(steps, step0 + kTurns) - 1;
+      if (last % L::kFlush == L::kFlush - 1 || last == steps - 1) {
+        wait_for(last);
         tc::fence_after_sync();
 #pragma unroll
         for (int j = 0; j < L::kSums; ++j) {
-          if (j > step % L::kFlush) break;
+          if (j > last % L::kFlush) break;
 #pragma unroll
-          for (int c = 0; c < kTall / 16; ++c) {
+          for (int c = 0; c < kHalf / 16; ++c) {
             float d[16];
-            tc::tmem_ld16(tmem + ((uint32_t)(32 * warp) << 16) + j * kTall + 16 * c, d);
+            tc::tmem_ld16(tmem + ((uint32_t)(32 * (warp % 4)) << 16) + j * kTall + row1 + 16 * c, d);
 #pragma unroll
             for (int r = 0; r < 16; ++r) total[16 * c + r] += d[r];
           }
@@ -854,8 +877,7 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
     __syncthreads();  // the stages are read by all: the sums go over them
     float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int r = 0; r < kTall; ++r)
-      if (tid < L::kSlots) sums[r * L::kSumStride + tid] = total[r];
+    for (int r = 0; r < kHalf; ++r) sums[(row1 + r) * L::kSumStride + tid % L::kSlots] = total[r];
     store_sums<BF16, L::kSlots>(p, sums, L::kSumStride, first, count, rank, group * L::kSlots,
                                 p.ad.scales ? __ldcg(p.ad.scales + a) : 1.f);
   }
@@ -1451,18 +1473,21 @@ struct ShrinkShape {
 int slots_of(const seedlm_adapters& ad) { return ad.rank <= 32 ? 32 : (ad.rank + 63) / 64 * 64; }
 
 // Whether a projection takes tiles of 8 rows or of 64.  In units of 57344 outputs
-// and inputs, a low tile was measured at 1.65 us whatever its rows and ranks, a
-// tall one at 3.75 us and 0.03 us a row, and its two kernels at 13 us more for
-// their longer start (8192 x 8192 and 28672+28672 x 8192, ranks 16 and 64, 1 to
-// 64 adapters, 16 to 2048 rows; e.g. 8 adapters of rank 64 on the larger: 41 us
-// low, 51 tall at 128 rows, 71 and 57 at 256).  The rows are taken to be spread
-// evenly over the adapters.
+// and inputs a low tile costs about 1 us and 0.03 us a slot (its ranks are read
+// and multiplied for eight rows only), a tall one 6 us and 0.05 us a row; the tall
+// form's two kernels take 9.5 us more to start.  Fitted to both forms' times at
+// 300 places (1 to 64 adapters of rank 8 to 128, 64 to 4096 rows, four shapes of
+// projections): the form taken is never more than 17 % behind the other, at any
+// of them.  One adapter, rank 8, 4096 inputs and outputs: low 11.1 us at 256 rows
+// and 21.9 at 1024, tall 13.6 and 18.8; rank 128, 8192 inputs, two slices of 28672
+// outputs, 64 rows: low 48.9, tall 29.7.  The tiles are counted as if the rows
+// were dealt evenly: how they are is on the device.
 bool takes_low_tiles(const seedlm_adapters& ad, int M) {
   double size = (double)ad.slices * ad.cols;
   for (int s = 0; s < ad.slices; ++s) size += ad.rows[s];
   const int used = std::min(M, ad.n), each = (M + used - 1) / used;
   const double low = (double)used * ((each + kLowRows - 1) / kLowRows), tall = (double)used * ((each + kTall - 1) / kTall);
-  return size / 57344 * (1.65 * low - 3.75 * tall - 0.03 * M) <= 13;
+  return size / 57344 * ((1 + 0.03 * slots_of(ad)) * low - 6 * tall - 0.05 * M) <= 9.5;
 }
 
 ShrinkShape shrink_shape(const seedlm_adapters& ad, int M, const DeviceInfo& dev) {
