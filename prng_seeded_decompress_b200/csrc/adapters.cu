@@ -694,7 +694,7 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
 // slots of the slices laid end to end (rows of A, the 128-row operand), each of
 // its CTAs one part of the columns, 64 at a time through a ring of shared-memory
 // stages.  Bound by the traffic from L2 (A again for every tile) and its latency:
-// 4096 rows, eight adapters of rank 64, two slices of 8192 columns: 200 MB in 33
+// 4096 rows, eight adapters of rank 64, two slices of 8192 columns: 200 MB in 28
 // us, 57 with the same products on mma.sync.  The tensor
 // cores cut off what an addition leaves below a sum's last bit, so the stages go
 // to four sums in turn, which after every 32 stages are added up in fp32, rounded.
@@ -1480,20 +1480,24 @@ int slots_of(const seedlm_adapters& ad) { return ad.rank <= 32 ? 32 : (ad.rank +
 // projections): the form taken is never more than 17 % behind the other, at any
 // of them.  One adapter, rank 8, 4096 inputs and outputs: low 11.1 us at 256 rows
 // and 21.9 at 1024, tall 13.6 and 18.8; rank 128, 8192 inputs, two slices of 28672
-// outputs, 64 rows: low 48.9, tall 29.7.  The tiles are counted as if the rows
-// were dealt evenly: how they are is on the device.
-bool takes_low_tiles(const seedlm_adapters& ad, int M) {
+// outputs, 64 rows: low 48.9, tall 29.7.  Where X or A is not aligned to 16 bytes
+// a low tile costs more: 1.3 leaves at most 21 % at 180 places (1: 49 %; four
+// adapters, rank 20, 4099 inputs and outputs, 512 rows: 32.0 low, 25.2 tall).
+// The tiles are counted as if the rows were dealt evenly: how they are is on the
+// device.
+bool takes_low_tiles(const seedlm_adapters& ad, int M, bool wide) {
+  const double low_cost = (1 + 0.03 * slots_of(ad)) * (wide ? 1 : 1.3);
   double size = (double)ad.slices * ad.cols;
   for (int s = 0; s < ad.slices; ++s) size += ad.rows[s];
   const int used = std::min(M, ad.n), each = (M + used - 1) / used;
   const double low = (double)used * ((each + kLowRows - 1) / kLowRows), tall = (double)used * ((each + kTall - 1) / kTall);
-  return size / 57344 * ((1 + 0.03 * slots_of(ad)) * low - 6 * tall - 0.05 * M) <= 9.5;
+  return size / 57344 * (low_cost * low - 6 * tall - 0.05 * M) <= 9.5;
 }
 
-ShrinkShape shrink_shape(const seedlm_adapters& ad, int M, const DeviceInfo& dev) {
+ShrinkShape shrink_shape(const seedlm_adapters& ad, int M, bool wide, const DeviceInfo& dev) {
   ShrinkShape sh{};
   sh.slots = slots_of(ad);
-  sh.low = takes_low_tiles(ad, M);
+  sh.low = takes_low_tiles(ad, M, wide);
   sh.tiles = max_tiles(M, ad.n, sh.low ? kLowRows : kTall);
   int64_t clusters = sh.tiles, round;
   if (sh.low) {
@@ -1648,7 +1652,7 @@ int launch_adapters_apply(const seedlm_adapters& ad, const int32_t* plan, int M,
     wide = wide && p.grain_a[s] == 16;
     wide_b = wide_b && p.grain_b[s] == 16;
   }
-  const ShrinkShape sh = shrink_shape(ad, M, dev);
+  const ShrinkShape sh = shrink_shape(ad, M, wide, dev);
   p.S = static_cast<uint16_t*>(workspace);
   p.unscale = reinterpret_cast<float*>(static_cast<char*>(workspace) + sums_bytes(ad, M, sh.slots));
   p.slots = sh.slots;

@@ -252,7 +252,8 @@ LOW = [
     (8, 256, [128], 1, 16), (9, 256, [128], 1, 64), (64, 512, [96, 40], 64, 20), (37, 1024, [256, 64, 64], 20, 16),
     (100, 300, [33, 1, 70, 31], 6, 37), (255, 96, [64], 300, 8), (256, 130, [130], 5, 130), (257, 130, [130], 5, 130),
     (300, 1000, [500], 1, 256), (333, 513, [127], 7, 12), (700, 64, [1000, 24], 3, 16), (1025, 264, [72], 1024, 4),
-    (17, 20000, [16], 2, 256), (600, 9001, [64], 2, 8), (64, 0, [40], 3, 8),
+    (17, 20000, [16], 2, 256), (600, 9001, [64], 2, 8), (64, 0, [40], 3, 8), (30, 2000, [300], 2, 256),
+    (60, 9001, [64], 2, 8),
 ]
 #: The same for batches that take tiles of 64 rows.
 TALL = [
