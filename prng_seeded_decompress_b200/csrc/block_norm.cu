@@ -660,21 +660,23 @@ __device__ __forceinline__ float activate(float g) {
   return g / (1.f + __expf(-1.5957691f * (g + 0.044715f * g * g * g)));
 }
 
-// Bound by memory: 2048 x 14336 in 44 us (6.7 TB/s).
+// Bound by memory: 2048 x 14336 in 44 us (6.7 TB/s).  Narrow rows share a CTA: a
+// CTA costs more to start than they do (3168 rows of 200: 6.9 us, 18.1 with one each).
 constexpr int kGluThreads = 256, kGluGroups = 2;  // groups of four outputs a thread
 
-template <int ACT, bool VEC>
+template <int ACT, bool VEC, bool NARROW>
 __global__ void __launch_bounds__(kGluThreads)
-glu_kernel(int cols, int chunks, const float* __restrict__ GU, int64_t ldgu, void* __restrict__ X, int64_t ldx, int x_dtype) {
+glu_kernel(int M, int cols, int chunks, const float* __restrict__ GU, int64_t ldgu, void* __restrict__ X, int64_t ldx, int x_dtype) {
   grid_launch_dependents();
-  const int64_t m = blockIdx.x / chunks;
-  const int first = (int)(blockIdx.x % chunks) * (4 * kGluThreads * kGluGroups);
+  const int64_t m = NARROW ? (int64_t)(blockIdx.x / chunks) * blockDim.y + threadIdx.y : blockIdx.x / chunks;
+  const int threads = NARROW ? blockDim.x : kGluThreads, first = (int)(blockIdx.x % chunks) * (4 * threads * kGluGroups);
   const float* G = GU + m * ldgu;
   grid_wait();
+  if (NARROW && m >= M) return;
   __align__(16) float g[kGluGroups][4], u[kGluGroups][4];
 #pragma unroll
   for (int i = 0; i < kGluGroups; ++i) {
-    const int j = first + (VEC ? 4 : 1) * (int)threadIdx.x + 4 * kGluThreads * i;
+    const int j = first + (VEC ? 4 : 1) * (int)threadIdx.x + 4 * threads * i;
     if (VEC) {
       if (j < cols) {
         *reinterpret_cast<float4*>(g[i]) = *reinterpret_cast<const float4*>(G + j);
@@ -683,15 +685,15 @@ glu_kernel(int cols, int chunks, const float* __restrict__ GU, int64_t ldgu, voi
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (j + kGluThreads * k < cols) {
-          g[i][k] = G[j + kGluThreads * k];
-          u[i][k] = G[cols + j + kGluThreads * k];
+        if (j + threads * k < cols) {
+          g[i][k] = G[j + threads * k];
+          u[i][k] = G[cols + j + threads * k];
         }
     }
   }
 #pragma unroll
   for (int i = 0; i < kGluGroups; ++i) {
-    const int j = first + (VEC ? 4 : 1) * (int)threadIdx.x + 4 * kGluThreads * i;
+    const int j = first + (VEC ? 4 : 1) * (int)threadIdx.x + 4 * threads * i;
     float v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = activate<ACT>(g[i][k]) * u[i][k];
@@ -703,7 +705,7 @@ glu_kernel(int cols, int chunks, const float* __restrict__ GU, int64_t ldgu, voi
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (j + kGluThreads * k < cols) store_as(X, m * ldx + j + kGluThreads * k, x_dtype, v[k]);
+        if (j + threads * k < cols) store_as(X, m * ldx + j + threads * k, x_dtype, v[k]);
     }
   }
 }
@@ -769,10 +771,14 @@ template <int ACT>
 int launch_glu_act(int M, int cols, const float* GU, int64_t ldgu, void* X, int64_t ldx, int x_dtype,
                    cudaStream_t stream) {
   const bool vec = cols % 4 == 0 && rows_of_four(GU, ldgu, SEEDLM_F32) && rows_of_four(X, ldx, x_dtype);
-  const int chunks = (cols + 4 * kGluThreads * kGluGroups - 1) / (4 * kGluThreads * kGluGroups);
-  if ((int64_t)M * chunks > INT32_MAX) return SEEDLM_EUNSUPPORTED;
-  auto kernel = vec ? glu_kernel<ACT, true> : glu_kernel<ACT, false>;
-  return launch_pdl(kernel, (unsigned)(M * chunks), kGluThreads, 0, stream, cols, chunks, GU, ldgu, X, ldx, x_dtype);
+  const int narrow = (cols + 127) / 128 * 32, rows = std::max(1, kGluThreads / narrow);
+  const int threads = rows > 1 ? narrow : kGluThreads;
+  const int64_t chunks = (cols + 4LL * threads * kGluGroups - 1) / (4 * threads * kGluGroups);
+  const int64_t grid = ((int64_t)M + rows - 1) / rows * chunks;
+  if (grid > INT32_MAX) return SEEDLM_EUNSUPPORTED;
+  auto kernel = rows > 1 ? (vec ? glu_kernel<ACT, true, true> : glu_kernel<ACT, false, true>)
+                         : (vec ? glu_kernel<ACT, true, false> : glu_kernel<ACT, false, false>);
+  return launch_pdl(kernel, (unsigned)grid, dim3(threads, rows), 0, stream, M, cols, (int)chunks, GU, ldgu, X, ldx, x_dtype);
 }
 
 }  // namespace

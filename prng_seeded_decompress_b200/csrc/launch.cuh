@@ -22,11 +22,11 @@ __device__ __forceinline__ void grid_launch_dependents() {
 }
 
 template <class... Params, class... Args>
-int launch_pdl_cluster(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+int launch_pdl_cluster(void (*kernel)(Params...), dim3 grid, dim3 threads, size_t smem, int cluster, cudaStream_t stream,
                        Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
+  cfg.blockDim = threads;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -47,7 +47,7 @@ int launch_pdl_cluster(void (*kernel)(Params...), dim3 grid, int threads, size_t
 }
 
 template <class... Params, class... Args>
-int launch_pdl(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream, Args&&... args) {
+int launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 threads, size_t smem, cudaStream_t stream, Args&&... args) {
   return launch_pdl_cluster(kernel, grid, threads, smem, 1, stream, std::forward<Args>(args)...);
 }
 
