@@ -437,6 +437,20 @@ def _run_on(device: int, stream, fn: str, call, *args):
         _check(fn, rc)
 
 
+def _made_for(stream, device: int):
+    """A context in which torch makes a call's own buffers for the stream that
+    the call runs on: what fills or used them before is then before the call,
+    and what gets their memory after is after it."""
+    import torch
+    if stream is not None and not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if stream is None or stream == torch.cuda.current_stream(device).cuda_stream:
+        return torch.cuda.device(device)
+    # (An ExternalStream of 0 would be a new stream.)
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream
+                             else torch.cuda.default_stream(device))
+
+
 class Adapters:
     """Low-rank adapters of one projection.
 
@@ -492,7 +506,9 @@ class AdapterPlan:
     """Room for the plan of a batch of M rows and n adapters.  After
     adapter_plan(): order (int32, M) holds the rows in the order of their
     adapter, those without one last; the rows of adapter a are
-    order[offsets[a]:offsets[a + 1]], offsets int32 (n + 1)."""
+    order[offsets[a]:offsets[a + 1]], offsets int32 (n + 1).  Made of zeros on
+    the current stream: as with any tensor, its first use on another stream has
+    to come after that."""
 
     def __init__(self, M: int, n: int, device=None):
         import torch
@@ -508,14 +524,16 @@ class AdapterPlan:
 def adapter_plan(ids, n: int, plan: AdapterPlan | None = None, stream=None) -> AdapterPlan:
     """Sort a batch's rows by adapter: ids int32 (M), a value outside 0..n-1
     for a row without one.  The result serves every adapter_apply() of the
-    batch; `plan` (for M rows and n adapters) is written again if given."""
+    batch; `plan` (for M rows and n adapters) is written again if given, else
+    one is made, on `stream` like the sort."""
     import torch
     if ids.dtype != torch.int32 or ids.dim() != 1:
         raise TypeError("ids must be a vector of int32")
     _dense(ids, "ids")
     M = ids.shape[0]
     if plan is None:
-        plan = AdapterPlan(M, n, device=ids.device)
+        with _made_for(stream, _place((ids,))):
+            plan = AdapterPlan(M, n, device=ids.device)
     elif plan.M != M or plan.n != n:
         raise ValueError(f"the plan is for {plan.M} rows and {plan.n} adapters, not {M} and {n}")
     _run_on(_place((ids, plan.buffer)), stream, "seedlm_adapters_plan", lib.seedlm_adapters_plan,
@@ -555,7 +573,8 @@ def adapter_apply(adapters: Adapters, plan: AdapterPlan, X, Y, base=None, worksp
     ldx = _rows_ld(X, (M, adapters.cols), "X")
     ldy = _f32_ld(Y, out, "Y")
     if workspace is None:
-        workspace = adapter_workspace(adapters, M)
+        with _made_for(stream, _place((X, Y))):
+            workspace = adapter_workspace(adapters, M)
     if base is None:
         ldb, pb, device = ldy, None, _place((X, Y, plan.buffer, workspace))
     else:
