@@ -184,6 +184,20 @@ def _dense(t, name: str):
     return t
 
 
+def _made_for(stream, device: int):
+    """A context in which torch makes a call's own buffers for the stream that
+    the call runs on: what fills or used them before is then before the call,
+    and what gets their memory after is after it."""
+    import torch
+    if stream is not None and not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if stream is None or stream == torch.cuda.current_stream(device).cuda_stream:
+        return torch.cuda.device(device)
+    # (An ExternalStream of 0 would be a new stream.)
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream
+                             else torch.cuda.default_stream(device))
+
+
 def init():
     _check("seedlm_init", lib.seedlm_init())
 
@@ -274,12 +288,14 @@ def gemm_workspace(fmt, M: int, device=None):
 def gemm_smallM(fmt, rec, eplane, X, Y, workspace=None, stream=None):
     """Y = X W^T; X float16/bfloat16 (M, cols), Y float32 (M, rows).
 
-    `workspace` comes from gemm_workspace(); if omitted a fresh one is made."""
+    `workspace` comes from gemm_workspace(); if omitted a fresh one is made for
+    `stream`."""
     f = _fmt(fmt)
     _dense(X, "X"), _dense(Y, "Y")
     M = int(X.shape[0])
     if workspace is None:
-        workspace = gemm_workspace(f, M, device=Y.device)
+        with _made_for(stream, Y.get_device()):
+            workspace = gemm_workspace(f, M, device=Y.device)
     nbytes = workspace.numel() * workspace.element_size()
     _check("seedlm_gemm_smallM", lib.seedlm_gemm_smallM(
         ctypes.byref(f), _ptr(rec), _ptr(eplane), _ptr(X), _act_dtype(X), M, _ptr(Y),
@@ -297,14 +313,15 @@ def gemm(fmt, rec, eplane, X, Y, workspace=None, stream=None):
     """Y = X W^T for any number of rows M of X (seedlm_gemm: passes of at most
     256 rows on the tensor cores; M = 1 runs the GEMV).  `workspace`: a
     zero-filled uint8 tensor of at least gemm_any_workspace_bytes(fmt, M)
-    bytes; if omitted a fresh one is made."""
+    bytes; if omitted a fresh one is made for `stream`."""
     import torch
     f = _fmt(fmt)
     _dense(X, "X"), _dense(Y, "Y")
     M = int(X.shape[0])
     if workspace is None:
-        workspace = torch.zeros(max(gemm_any_workspace_bytes(f, M), 256), dtype=torch.uint8,
-                                device=Y.device)
+        with _made_for(stream, Y.get_device()):
+            workspace = torch.zeros(max(gemm_any_workspace_bytes(f, M), 256), dtype=torch.uint8,
+                                    device=Y.device)
     nbytes = workspace.numel() * workspace.element_size()
     _check("seedlm_gemm", lib.seedlm_gemm(
         ctypes.byref(f), _ptr(rec), _ptr(eplane), _ptr(X), _act_dtype(X), M, _ptr(Y),
@@ -435,20 +452,6 @@ def _run_on(device: int, stream, fn: str, call, *args):
             rc = call(*args, stream)
     if rc != 0:
         _check(fn, rc)
-
-
-def _made_for(stream, device: int):
-    """A context in which torch makes a call's own buffers for the stream that
-    the call runs on: what fills or used them before is then before the call,
-    and what gets their memory after is after it."""
-    import torch
-    if stream is not None and not isinstance(stream, int):
-        stream = stream.cuda_stream
-    if stream is None or stream == torch.cuda.current_stream(device).cuda_stream:
-        return torch.cuda.device(device)
-    # (An ExternalStream of 0 would be a new stream.)
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream
-                             else torch.cuda.default_stream(device))
 
 
 class Adapters:

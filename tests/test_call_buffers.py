@@ -5,9 +5,12 @@ torch's streams replaced by names; on the GPU with the other stream kept busy,
 so that a buffer of the wrong stream would be filled, or used by others, at the
 wrong time."""
 import contextlib
+import types
 
 import numpy as np
 import pytest
+
+from prng_seeded_decompress_b200 import inputs
 
 torch = pytest.importorskip("torch")
 
@@ -85,6 +88,21 @@ def test_a_plan_and_a_workspace_are_made_on_the_calls_stream(sl, made_on, stream
     assert made_on(calls) == [handle, handle]
 
 
+@pytest.mark.parametrize("stream,handle", [(None, 7), (FakeStream(9), 9), (9, 9), (7, 7), (0, 0)])
+def test_a_products_workspace_is_made_on_the_calls_stream(sl, made_on, monkeypatch, stream, handle):
+    fmt = inputs.make_layer(64, 128, 8, 3, seed=1)["fmt"]
+    rec, X, Y = torch.zeros(64, 16, dtype=torch.int32), torch.zeros(20, 128).half(), torch.zeros(20, 64)
+    monkeypatch.setattr(sl, "gemm_workspace_bytes", lambda f, M: 1000)
+    monkeypatch.setattr(sl, "gemm_any_workspace_bytes", lambda f, M: 1000)
+    monkeypatch.setattr(sl, "_check", lambda fn, rc: None)
+    monkeypatch.setattr(sl, "lib", types.SimpleNamespace(seedlm_gemm=lambda *a: 0, seedlm_gemm_smallM=lambda *a: 0))
+
+    def calls():
+        sl.gemm(fmt, rec, None, X, Y, stream=stream)
+        sl.gemm_smallM(fmt, rec, None, X, Y, stream=stream)
+    assert made_on(calls) == [handle, handle]
+
+
 def batch(M, seed):
     g = torch.Generator().manual_seed(seed)
     whole = lambda *s: torch.randint(-2, 3, s, generator=g)  # noqa: E731
@@ -128,3 +146,25 @@ def test_a_workspace_made_by_a_call_is_not_the_current_streams(gpu, M):
     torch.cuda.synchronize()
     assert bool((mine == 255).all())
     assert torch.equal(Y.cpu().double(), ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [16, 600])
+def test_a_products_workspace_is_cleared_before_the_product(gpu, oracle_mod, M):
+    L = inputs.make_layer(256, 512, 8, 3, seed=M)
+    W = torch.from_numpy(oracle_mod.decompress(L["fmt"], L["rec"], None)).double()
+    rec = torch.from_numpy(L["rec"].view(np.int32)).cuda()
+    X = torch.randn(M, 512, generator=torch.Generator().manual_seed(M)).half()
+    Xd, side = X.cuda(), torch.cuda.Stream()
+    size = gpu.gemm_any_workspace_bytes(L["fmt"], M)
+    for call in (gpu.gemm, gpu.gemm_smallM)[:2 if M <= 64 else 1]:
+        Y = torch.full((M, 256), float("nan"), device="cuda")
+        with torch.cuda.stream(side):  # memory that the workspace may come to lie in
+            torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        torch.cuda._sleep(BUSY)
+        call(L["fmt"], rec, None, Xd, Y, stream=side)
+        side.synchronize()
+        torch.cuda.synchronize()
+        ref = X.double() @ W.T
+        assert bool(((Y.cpu().double() - ref).abs() <= 1e-5 * (X.double().abs() @ W.abs().T)).all())
