@@ -320,9 +320,13 @@ SEEDLM_API int64_t seedlm_adapters_plan_words(int32_t M, int32_t n);
  * leading dimensions ldb and ldy.  base == NULL or base == Y (then with
  * ldb == ldy) adds in place, and rows without an adapter are neither read
  * nor written; a base that overlaps Y in another way gives undefined
- * results.  plan: made by seedlm_adapters_plan for this M and ad->n; memory of
- * that size that holds anything else (a plan of others, zeros) changes nothing
- * in Y and sets value 4 of seedlm_device_error.  Sums are fp32 in a fixed order per shape; x A^T is
+ * results.  plan: made by seedlm_adapters_plan from this batch's ids, for this M
+ * and ad->n.  One made for another M or n, and zeros, are found out: nothing in
+ * Y changes, and value 4 of seedlm_device_error is set.  A plan of another
+ * batch with the same M and n is followed.  Memory of that size that was written
+ * over since leads to no access outside the arrays, but to undefined rows of Y;
+ * value 4 is set where it names rows, adapters or tiles that there are none of.
+ * Sums are fp32 in a fixed order per shape; x A^T is
  * kept to 24 bits between the two products.  Any alignment of X, A, B, base
  * and Y that their types allow is accepted; arrays whose rows all begin at
  * multiples of 16 bytes are read fastest.  `workspace`: device memory of at least
@@ -397,7 +401,8 @@ SEEDLM_API int seedlm_selftest_wait_timeout(int64_t limit_ns, seedlm_stream stre
  * memory index outside the buffers its arguments describe, or a
  * shared-memory index outside its launch's allocation, and skipped that
  * access, bit 2 (value 4) if seedlm_adapters_apply was given a plan made for
- * another batch size or number of adapters and changed nothing.  The outputs
+ * another batch size or number of adapters and changed nothing, or one that was
+ * written over and skipped what cannot be followed.  The outputs
  * of such a call are undefined.  0 if nothing happened.
  * HOST function; synchronous. */
 SEEDLM_API int seedlm_device_error(int* flag);

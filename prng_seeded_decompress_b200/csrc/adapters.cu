@@ -18,7 +18,7 @@ SEEDLM_CHECK_FLAG(adapters)
 
 namespace {
 
-// Set when a plan does not belong to the call it is given to.
+// Set when a plan does not belong to the call it is given to, or was written over.
 __device__ unsigned int g_plan_mismatch;
 // Set when a kernel gave up waiting for its own products.
 __device__ unsigned int g_wait_error;
@@ -27,11 +27,14 @@ __device__ unsigned int g_wait_error;
 //
 // Layout in int32 words: [0, M) order, [M, M + n + 1) offsets, then from the
 // next multiple of 4, for tiles of up to 8 rows and for tiles of up to 64, a head
-// {M, n, tiles of rows with an adapter, all tiles}; then for each of the two an
+// {M + mark, n, tiles of rows with an adapter, all tiles}; then for each of the two an
 // int4 {adapter or -1, first, count, 0} for every tile, in sorted order.  Each
-// projection takes the one that suits it.
+// projection takes the one that suits it.  The mark is larger than any other
+// word of a plan, so that no part of another plan looks like a head.
 
 constexpr int kLowRows = 8, kTall = 64;
+constexpr int kHeadMark = 0x5e000000;
+static_assert(kMaxAdapterRows < 0x02000000 && (kHeadMark & 0x01ffffff) == 0, "M fits below the mark");
 
 __host__ __device__ inline int64_t plan_tail(int64_t M, int64_t n) { return (M + n + 1 + 3) / 4 * 4; }
 
@@ -209,7 +212,7 @@ adapters_plan_kernel(int M, int n, const int32_t* __restrict__ ids, int32_t* __r
   int4* tail = reinterpret_cast<int4*>(plan + plan_tail(M, n));
   auto list = [&](int T, const int32_t* first, int4* head, int4* to) {
     const int all = first[bins];
-    if (cta == 0 && threadIdx.x == 0) *head = make_int4(M, n, first[n], all);
+    if (cta == 0 && threadIdx.x == 0) *head = make_int4(kHeadMark + M, n, first[n], all);
     for (int t = cta * blockDim.x + threadIdx.x; t < all; t += ctas * blockDim.x) {
       int lo = 0, hi = bins - 1;  // the last bin that starts at or before tile t
       while (lo < hi) {
@@ -257,6 +260,7 @@ struct ApplyArgs {
   seedlm_adapters ad;
   const int32_t* plan;
   const int4 *head, *tiles;  // the plan's, of the tiles that are taken
+  int room;         // tiles that the plan has room for
   int M;
   const uint16_t* X;
   int64_t ldx;
@@ -277,12 +281,15 @@ struct ApplyArgs {
   int grain_x, grain_a[SEEDLM_MAX_SLICES], grain_b[SEEDLM_MAX_SLICES], grain_y[SEEDLM_MAX_SLICES];
 };
 
-// The plan's head, {M, n, tiles with an adapter, tiles}, with no tiles at all if
-// it does not belong to this call.
+// What a plan says is checked before it is followed: memory that holds something
+// else is reported and leads to no access outside the arrays.
+__device__ __forceinline__ void plan_is_wrong() { atomicOr(&g_plan_mismatch, 1u); }
+
+// The plan's head, with no tiles at all if it does not belong to this call.
 __device__ __forceinline__ int4 plan_head(const ApplyArgs& p) {
   int4 head = __ldcg(p.head);
-  if (head.x != p.M || head.y != p.ad.n) {
-    if (threadIdx.x == 0) atomicOr(&g_plan_mismatch, 1u);
+  if (head.x != kHeadMark + p.M || head.y != p.ad.n || (unsigned)head.w > (unsigned)p.room || (unsigned)head.z > (unsigned)head.w) {
+    if (threadIdx.x == 0) plan_is_wrong();
     head.z = head.w = 0;
   }
   return head;
@@ -293,6 +300,23 @@ __device__ __forceinline__ int4 plan_head(const ApplyArgs& p) {
 __device__ __forceinline__ int4 plan_tile(const ApplyArgs& p, int64_t t) {
   return __ldcg(p.tiles + t);
 }
+
+// Whether it is a tile of at most T rows of this batch, with an adapter from
+// `least` on.
+__device__ __forceinline__ bool tile_fits(const ApplyArgs& p, const int4& tile, int T, int least) {
+  const bool fits = tile.x >= least && tile.x < p.ad.n && tile.z >= 0 && tile.z <= T && tile.y >= 0 && tile.y <= p.M - tile.z;
+  if (!fits && threadIdx.x == 0) plan_is_wrong();
+  return fits;
+}
+
+// A row's number as the plan has it, -1 if there is no such row.
+__device__ __forceinline__ int row_of(const ApplyArgs& p, int row) {
+  if ((unsigned)row < (unsigned)p.M) return row;
+  plan_is_wrong();
+  return -1;
+}
+// The row at place i of the batch in sorted order.
+__device__ __forceinline__ int plan_row(const ApplyArgs& p, int i) { return row_of(p, __ldcg(p.plan + i)); }
 
 __device__ __forceinline__ int rank_of(const seedlm_adapters& ad, int a) {
   if (a < 0) return 0;
@@ -569,16 +593,21 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
   if (t >= head.z) return;
   const int a = tile.x, first = tile.y, count = tile.z;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, q = lane % 4;
-  const int row = g < count ? __ldcg(p.plan + first + g) : -1;
-  const int r0 = group * R, rank = rank_of(p.ad, a) - r0;  // of this group
-  const float scale = p.ad.scales ? __ldcg(p.ad.scales + a) : 1.f;
+  // Asked for, at places that there are, before the tile is looked at (37 rows, 20
+  // adapters, q, k, v of 4096 columns: 9.0 us, 9.2 after it).
+  const int named = __ldcg(p.plan + min((unsigned)first + g, (unsigned)p.M - 1));
+  const int some = (int)min((unsigned)a, (unsigned)p.ad.n - 1);
+  const int r0 = group * R, rank = rank_of(p.ad, some) - r0;  // of this group
+  const float scale = p.ad.scales ? __ldcg(p.ad.scales + some) : 1.f;
+  if (!tile_fits(p, tile, kLowRows, 0)) return;  // the same in all CTAs of a cluster
+  const int row = g < count ? row_of(p, named) : -1;
   if (rank <= 0 || p.ad.rows[s] == 0) return;
   const int k0 = (int)cluster_rank() * p.split_cols, k1 = min(p.ad.cols, k0 + p.split_cols);
   const int blocks = min(RB, (rank + 15) / 16);
 
   // Row g of the tile and rows 8 j + g of A, at this lane's place in the part.
   const int64_t a_row = p.ad.a_row[s];
-  const bool have_x = row >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, row, p.M);
+  const bool have_x = row >= 0;
   const int k_first = k0 + warp * kStep + 8 * q;
   const uint16_t* x = p.X + (have_x ? row * p.ldx : 0) + k_first;
   const uint16_t* A = static_cast<const uint16_t*>(p.ad.A[s]) + a * p.ad.a_adapter[s] + r0 * a_row + k_first;
@@ -742,7 +771,7 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
   const int group = cluster % p.groups, t = cluster / p.groups;
   const int4 tile = plan_tile(p, t), head = plan_head(p);
   bool ok = true;
-  if (t < head.z) {  // the same in all CTAs of a cluster
+  if (t < head.z && tile_fits(p, tile, kTall, 0)) {  // the same in all CTAs of a cluster
     const int a = tile.x, first = tile.y, count = tile.z;
     const int rank = rank_of(p.ad, a);
     const int k0 = (int)cluster_rank() * p.split_cols, k1 = min(p.ad.cols, k0 + p.split_cols);
@@ -758,19 +787,19 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
     const uint16_t* src[kMine];
     unsigned there = 0;
     // The row's first element; null: no such row.
-    auto row_of = [&](int i) -> const uint16_t* {
+    auto row_at = [&](int i) -> const uint16_t* {
       const int row = row0 + kApart * i;
       if (row < L::kSlots) {
         const int place_of = group * L::kSlots + row, s = place_of / p.slots, r = place_of - s * p.slots;
         if (s >= p.ad.slices || r >= rank || p.ad.rows[s] == 0) return nullptr;
         return static_cast<const uint16_t*>(p.ad.A[s]) + a * p.ad.a_adapter[s] + r * p.ad.a_row[s];
       }
-      const int m = row - L::kSlots < count ? __ldcg(p.plan + first + row - L::kSlots) : -1;
-      return m >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, m, p.M) ? p.X + m * p.ldx : nullptr;
+      const int m = row - L::kSlots < count ? plan_row(p, first + row - L::kSlots) : -1;
+      return m >= 0 ? p.X + m * p.ldx : nullptr;
     };
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
-      src[i] = row_of(i);
+      src[i] = row_at(i);
       there |= (unsigned)(src[i] != nullptr) << i;
       if (!src[i])
         for (int st = 0; st < L::kStages; ++st)
@@ -800,7 +829,7 @@ adapters_shrink_tall_kernel(const __grid_constant__ ApplyArgs p) {
 #pragma unroll 1
             for (int i = 0; i < kMine; ++i)
               if (there >> i & 1) {
-                const uint16_t* from = row_of(i) + k;
+                const uint16_t* from = row_at(i) + k;
                 copy_raw(extent_of(i), to + i * kRaw2, from, checked(extent_of(i), from, have), kRaw2 / 2);
               }
           }
@@ -922,7 +951,7 @@ struct ExpandTile {
 __device__ __forceinline__ bool expand_tile(const ApplyArgs& p, int chunks, int in_place, ExpandTile& x) {
   const int t = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
   const int4 tile = plan_tile(p, t), head = plan_head(p);
-  if (t >= (in_place ? head.z : head.w)) return false;
+  if (t >= (in_place ? head.z : head.w) || !tile_fits(p, tile, kLowRows, -1)) return false;
   x.a = tile.x;
   x.first = tile.y;
   x.count = tile.z;
@@ -968,8 +997,8 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
   float* to[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const int m = 2 * q + e < x.count ? __ldcg(p.plan + x.first + 2 * q + e) : -1;
-    const bool ok = m >= 0 && SEEDLM_IN_BOUNDS(g_check_flag, m, p.M);
+    const int m = 2 * q + e < x.count ? plan_row(p, x.first + 2 * q + e) : -1;
+    const bool ok = m >= 0;
     from[e] = ok ? p.base + m * p.ldb + p.slice_at[x.s] + 4 * g : nullptr;
     to[e] = ok ? p.Y + m * p.ldy + p.slice_at[x.s] + 4 * g : nullptr;
   }
@@ -1209,6 +1238,7 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
     while (chunk >= p.chunk_first[s + 1]) ++s;
     const int items = (int)min(end - item, (int64_t)(p.chunk_first[s + 1] - chunk));
     item += items;
+    if (!tile_fits(p, tile, T, -1)) continue;
     const int rank = rank_of(p.ad, a);
     if (in_place && rank == 0) continue;
     const int rows = p.ad.rows[s], c0 = (chunk - p.chunk_first[s]) * kOut;
@@ -1217,11 +1247,12 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
     const bool pairs = p.grain_y[s] >= 8;
     const bool products = rank > 0;
     __syncthreads();  // the tile before is done with shared memory
+    bool wrong = false;
     if (tid < T) {
-      const int m = tid < count ? __ldcg(p.plan + first + tid) : 0;
-      const bool in = SEEDLM_IN_BOUNDS(g_check_flag, m, p.M);
-      from_row[tid] = (in ? m * p.ldb : 0) + p.slice_at[s];
-      to_row[tid] = (in ? m * p.ldy : 0) + p.slice_at[s];
+      const int m = tid < count ? plan_row(p, first + tid) : 0;
+      wrong = m < 0;
+      from_row[tid] = m * p.ldb + p.slice_at[s];
+      to_row[tid] = m * p.ldy + p.slice_at[s];
     }
     // B of outputs c0 + 256 i + (0 .. 255): output 2 j + h is row j of half h, or,
     // where base and Y cannot be read in pairs, output 128 h + j.
@@ -1357,7 +1388,7 @@ adapters_expand_tall_kernel(const __grid_constant__ ApplyArgs p, int chunks, int
     copies_wait<0>();
     tc::fence_proxy_async();
     tc::fence_before_sync();  // of the sums before, read
-    __syncthreads();
+    if (__syncthreads_or(wrong)) continue;  // (a plan that was written over)
     tc::fence_after_sync();
     if (products && warp == 0) multiply();
     ask(0, 0);
@@ -1660,6 +1691,7 @@ int launch_adapters_apply(const seedlm_adapters& ad, const int32_t* plan, int M,
   p.split_cols = sh.split_cols;
   p.groups = sh.groups;
   const int64_t tiles = sh.tiles;
+  p.room = (int)tiles;
   p.head = reinterpret_cast<const int4*>(plan + plan_tail(M, ad.n)) + (sh.low ? 0 : 1);
   p.tiles = reinterpret_cast<const int4*>(plan + plan_tail(M, ad.n)) + 2 + (sh.low ? 0 : max_tiles(M, ad.n, kLowRows));
   if (tiles * ad.slices * sh.groups * sh.splits > INT32_MAX) return SEEDLM_EUNSUPPORTED;

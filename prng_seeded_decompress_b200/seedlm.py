@@ -342,7 +342,9 @@ def gemm_smallM_noalloc(fmt, rec, eplane, X, Y, stream=None):
 def device_error() -> int:
     """Reads and clears the device error flags: bit 0 if a kernel gave up on
     one of its own bounded waits, bit 1 if a kernel of the checked build
-    skipped an out-of-bounds access.  Synchronous."""
+    skipped an out-of-bounds access, bit 2 (value 4) if adapter_apply() was given
+    a plan made for another batch size or number of adapters, or one that was
+    written over.  Synchronous."""
     flag = ctypes.c_int(0)
     _check("seedlm_device_error", lib.seedlm_device_error(ctypes.byref(flag)))
     return int(flag.value)
