@@ -80,7 +80,7 @@ __device__ __forceinline__ int load_of_cta(const int* mine, uint32_t cta) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1)
-adapters_plan_kernel(int M, int n, const int32_t* __restrict__ ids, int32_t* __restrict__ plan) {
+adapters_plan_kernel(int M, int n, const int32_t* ids, int32_t* plan) {
   extern __shared__ int32_t sm[];
   const int bins = n + 1, nwarps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cta = (int)cluster_rank(), ctas = (int)cluster_size();
@@ -435,7 +435,7 @@ __device__ __forceinline__ void copy_raw(const Extent& m, unsigned char* to, con
   } else {
     uint16_t e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = i < have ? __ldg(from + i) : (uint16_t)0;
+    for (int i = 0; i < 8; ++i) e[i] = i < have ? from[i] : (uint16_t)0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       *reinterpret_cast<uint16_t*>(to + (off + i >= 8 ? second - 16 : 0) + 2 * (off + i)) = e[i];
@@ -461,11 +461,11 @@ __device__ __forceinline__ uint4 load_unit(const Extent& m, const uint16_t* from
   const int off = off_of(from);
   if (words_inside(m, from)) {
     const uint4* at = reinterpret_cast<const uint4*>(from - off);
-    return shift_unit(__ldg(at), __ldg(at + 1), off, have);
+    return shift_unit(at[0], at[1], off, have);
   }
   uint16_t e[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) e[i] = i < have ? __ldg(from + i) : (uint16_t)0;
+  for (int i = 0; i < 8; ++i) e[i] = i < have ? from[i] : (uint16_t)0;
   return make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16,
                     e[6] | (uint32_t)e[7] << 16);
 }

@@ -666,7 +666,7 @@ constexpr int kGluThreads = 256, kGluGroups = 2;  // groups of four outputs a th
 
 template <int ACT, bool VEC, bool NARROW>
 __global__ void __launch_bounds__(kGluThreads)
-glu_kernel(int M, int cols, int chunks, const float* __restrict__ GU, int64_t ldgu, void* __restrict__ X, int64_t ldx, int x_dtype) {
+glu_kernel(int M, int cols, int chunks, const float* GU, int64_t ldgu, void* X, int64_t ldx, int x_dtype) {
   grid_launch_dependents();
   const int64_t m = NARROW ? (int64_t)(blockIdx.x / chunks) * blockDim.y + threadIdx.y : blockIdx.x / chunks;
   const int threads = NARROW ? blockDim.x : kGluThreads, first = (int)(blockIdx.x % chunks) * (4 * threads * kGluGroups);

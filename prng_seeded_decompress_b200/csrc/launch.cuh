@@ -1,6 +1,9 @@
 // launch.cuh -- launching kernels with programmatic dependent launch: the
 // kernel may start while the one before it on the stream is finishing, and
-// calls grid_wait() before it reads or writes anything that kernel touches.
+// calls grid_wait() before it reads or writes anything that kernel touches.  What
+// that kernel may write is not constant for the life of this one: it is read with
+// plain loads, not through the read-only path (__ldg, or a kernel's own const
+// __restrict__ pointers), which the compiler may also move above the wait.
 #pragma once
 
 #include <cuda_runtime.h>
