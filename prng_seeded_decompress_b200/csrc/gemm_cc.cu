@@ -105,7 +105,7 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p) {
 // X columns of spans [s0, s0 + sl), zero past cols and past M rows, into the
 // segment's slots.  One thread per (unit, row of X).
 template <int C, int MB>
-__device__ void stage_x(float* xs, const uint16_t* __restrict__ X, int is_bf16, const CcGeom& g,
+__device__ void stage_x(float* xs, const uint16_t* X, int is_bf16, const CcGeom& g,
                         int s0, int sl, int vec) {
   const int units = sl * kSpan;
   SEEDLM_CHECK_ONLY(const unsigned int xs_floats = CcSmem<C, MB>::kXBytes / 4;)
@@ -193,7 +193,7 @@ __device__ __forceinline__ void rebuild_and_dot(const CcRecs<R>& cur, const floa
 template <int C, int MB>
 __global__ void __launch_bounds__(kWarps * 32, 1)
 gemm_cc_kernel(const uint32_t* __restrict__ rec, const uint8_t* __restrict__ eplane,
-               const uint16_t* __restrict__ X, int is_bf16, int vec, float* __restrict__ Y,
+               const uint16_t* X, int is_bf16, int vec, float* __restrict__ Y,
                const __grid_constant__ CcGeom g) {
   using S = CcSmem<C, MB>;
   constexpr int kE = S::kEntries;

@@ -364,7 +364,7 @@ struct RecUnit {
 template <int C, int NB>
 __global__ void __launch_bounds__(Roles<C>::kThreads, 1)
 gemm_tc_kernel(const uint32_t* __restrict__ rec, const uint8_t* __restrict__ eplane,
-               const unsigned char* __restrict__ Xs, const float2* __restrict__ yscale,
+               const unsigned char* Xs, const float2* yscale,
                float* __restrict__ Y, float* __restrict__ partial,
                unsigned int* __restrict__ counters, TcGeom g) {
   using L = TcSmem<C, NB>;

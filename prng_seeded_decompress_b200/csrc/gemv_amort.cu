@@ -107,7 +107,7 @@ struct StripIn {
 
 __device__ __forceinline__ void load_strip(StripIn& o, const uint32_t* __restrict__ rec,
                                            const uint8_t* __restrict__ eplane,
-                                           const uint16_t* __restrict__ x, const AmortGeom& g, int r0,
+                                           const uint16_t* x, const AmortGeom& g, int r0,
                                            int r1, int warp, int lane, int s) {
   const int u = s * kStrip + lane;
 #pragma unroll
@@ -234,7 +234,7 @@ __device__ __forceinline__ float block_dot(uint32_t rec, uint32_t e4, float xsum
 
 __global__ void __launch_bounds__(kWarps * 32, 1)
 gemv_amort_kernel(const uint32_t* __restrict__ rec, const uint8_t* __restrict__ eplane,
-                  const uint16_t* __restrict__ x, int is_bf16, float* __restrict__ y,
+                  const uint16_t* x, int is_bf16, float* __restrict__ y,
                   const __grid_constant__ AmortGeom g) {
   extern __shared__ __align__(16) unsigned char smem[];
   // The next kernel in the stream may launch now; its CTAs take an SM when
