@@ -652,11 +652,36 @@ __global__ void __launch_bounds__(kWideThreads) block_norm_wide_kernel(const __g
 
 // ---------------------------------------------------------------------- glu
 
+// The larger part of erf GELU's work: g/2 (1 + erf(g / sqrt 2)) = max(g, 0) -
+// |g| Q(|g|) with Q(m) = erfc(m / sqrt 2) / 2, which keeps the relative accuracy
+// of the negative tail, where the sum cancels.  Q(m) = e^(-m^2/2) t P(t), t =
+// 1 / (1 + 0.35 m), the form of Hastings' approximations (Abramowitz and Stegun
+// 7.1.26); P is a minimax fit of degree 8, made in 64 bits for m up to 13.3 (where
+// e^(-m^2/2) leaves fp32), off by 3.2e-8 at most.  With the roundings of fp32, of
+// the reciprocal and of the exponential GELU is off by less than (g^2 + 9) 2^-23
+// of its value below 0.  2048 x 14336: 43 us, 60 with erfcf, 44 with
+// 1 + erff(g / sqrt 2), which is 10 % off at -5.
+__device__ __forceinline__ float gelu(float g) {
+  const float m = fminf(fabsf(g), 30.f);  // Q is 0 from there on, at infinity too
+  const float t = __fdividef(1.f, fmaf(0.35f, m, 1.f));
+  float p = -0.029114645f;
+  p = fmaf(p, t, 0.143816575f);
+  p = fmaf(p, t, -0.255387127f);
+  p = fmaf(p, t, 0.158792019f);
+  p = fmaf(p, t, -0.0228402093f);
+  p = fmaf(p, t, 0.105390742f);
+  p = fmaf(p, t, 0.119863458f);
+  p = fmaf(p, t, 0.139857516f);
+  p = fmaf(p, t, 0.13962166f);
+  const float q = t * p * __expf(-0.5f * m * m);
+  return fmaf(-m, q, g < 0.f ? 0.f : g);  // (NaN stays)
+}
+
 // The sigmoid form of the tanh one: (1 + tanh z) / 2 = 1 / (1 + e^-2z).
 template <int ACT>
 __device__ __forceinline__ float activate(float g) {
   if (ACT == SEEDLM_SILU) return g / (1.f + __expf(-g));
-  if (ACT == SEEDLM_GELU) return 0.5f * g * (1.f + erff(g * 0.70710678f));
+  if (ACT == SEEDLM_GELU) return gelu(g);
   return g / (1.f + __expf(-1.5957691f * (g + 0.044715f * g * g * g)));
 }
 
