@@ -396,8 +396,9 @@ def _bind_torch():
     global _raw_stream, _current_device
     import torch
     _CODES.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
-    _raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream() makes an object
     _current_device = torch._C._cuda_getDevice
+    # Last, as _run_on() of another thread goes by it (current_stream() makes an object).
+    _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _any_dtype(t) -> int:
