@@ -410,6 +410,13 @@ def _any_dtype(t) -> int:
     return code
 
 
+def _fits(what: str, *sizes):
+    """Sizes that the library takes as 32-bit numbers (ctypes would cut them off)."""
+    for v in sizes:
+        if not -1 << 31 <= v < 1 << 31:
+            raise ValueError(f"{what} must fit in 32 bits, got {v}")
+
+
 def _rows_ld(t, shape: tuple, name: str) -> int:
     """Leading dimension of a matrix argument of this shape with unit column stride."""
     if t.shape != shape:
@@ -483,6 +490,7 @@ class Adapters:
             if (a.shape[2] > 1 and a.stride(2) != 1) or (b.shape[2] > 1 and b.stride(2) != 1):
                 raise ValueError("A and B must have unit stride in their last dimension")
         n, rank, cols = (int(v) for v in A[0].shape)
+        _fits("sizes of A and B", n, rank, cols, *(int(b.shape[1]) for b in B))
         for t, name, dt in ((ranks, "ranks", torch.int32), (scales, "scales", torch.float32)):
             if t is None:
                 continue
@@ -518,6 +526,7 @@ class AdapterPlan:
 
     def __init__(self, M: int, n: int, device=None):
         import torch
+        _fits("rows and adapters", int(M), int(n))
         words = int(lib.seedlm_adapters_plan_words(int(M), int(n)))
         if words < 0:
             _check("seedlm_adapters_plan_words", words)
@@ -538,6 +547,7 @@ def adapter_plan(ids, n: int, plan: AdapterPlan | None = None, stream=None) -> A
     _dense(ids, "ids")
     M = ids.shape[0]
     if plan is None:
+        _fits("rows and adapters", M, n)
         with _made_for(stream, _place((ids,))):
             plan = AdapterPlan(M, n, device=ids.device)
     elif plan.M != M or plan.n != n:
@@ -548,6 +558,7 @@ def adapter_plan(ids, n: int, plan: AdapterPlan | None = None, stream=None) -> A
 
 
 def adapter_workspace_bytes(adapters: Adapters, M: int) -> int:
+    _fits("rows", int(M))
     n = int(lib.seedlm_adapters_workspace_bytes(adapters.ref, int(M)))
     if n < 0:
         _check("seedlm_adapters_workspace_bytes", n)
@@ -615,6 +626,7 @@ class BlockNorm:
                 raise ValueError(f"weights and biases must have {cols} entries")
             _dense(t, "a weight or bias")
         self.cols = int(cols)
+        _fits("cols", self.cols)
         self.tensors = given
         self.device = given[0].get_device() if given else -1
         if any(t.get_device() != self.device for t in given):
@@ -638,6 +650,8 @@ def block_norm(norm: BlockNorm, y, h, h_out=None, x=None, gate=None, stream=None
         raise ValueError("y or h, and h_out or x, must be given")
     cols = norm.cols
     shape = (like.shape[0] if like.dim() else 0, cols)
+    if shape[0] >> 31:
+        _fits("rows", shape[0])
     tensors = []
     ldy = ldg = ldh = ldo = ldx = ht = xt = 0
     py = pg = ph = po = px = None
@@ -687,6 +701,8 @@ def glu(GU, X, act: str = "silu", stream=None):
     if X.dim() != 2:
         raise ValueError("X must be M x cols")
     M, cols = X.shape
+    if (M | cols) >> 31:
+        _fits("rows and columns", M, cols)
     ldx, xt = _rows_ld(X, (M, cols), "X"), _any_dtype(X)
     if xt == F32:
         raise TypeError("X must be float16 or bfloat16, got float32")
