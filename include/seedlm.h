@@ -326,13 +326,15 @@ SEEDLM_API int64_t seedlm_adapters_plan_words(int32_t M, int32_t n);
  * batch with the same M and n is followed.  Memory of that size that was written
  * over since leads to no access outside the arrays, but to undefined rows of Y;
  * value 4 is set where it names rows, adapters or tiles that there are none of.
- * Sums are fp32 in a fixed order per shape; x A^T is
- * kept to 24 bits between the two products.  Any alignment of X, A, B, base
- * and Y that their types allow is accepted; arrays whose rows all begin at
- * multiples of 16 bytes are read fastest.  `workspace`: device memory of at least
- * seedlm_adapters_workspace_bytes(ad, M) bytes, 256-byte aligned, of any
- * content; calls that share one must not run concurrently (calls on one
- * stream never do). */
+ * Sums are fp32 in a fixed order per shape and alignment.  Between the two
+ * products x A^T is kept to 24 bits with bf16; with fp16 to 2^-23 of the value,
+ * or to 2^-39 of the largest among the row's 64 ranks where that is more.  An
+ * infinite entry of B gives an infinity or NaN in its output.
+ * Any alignment of X, A, B, base and Y that their types allow is accepted;
+ * arrays whose rows all begin at multiples of 16 bytes are read fastest.
+ * `workspace`: device memory of at least seedlm_adapters_workspace_bytes(ad, M)
+ * bytes, 256-byte aligned, of any content; calls that share one must not run
+ * concurrently (calls on one stream never do). */
 SEEDLM_API int seedlm_adapters_apply(const seedlm_adapters* ad, const int32_t* plan, int32_t M,
                                      const void* X, int64_t ldx, const float* base, int64_t ldb,
                                      float* Y, int64_t ldy, void* workspace,

@@ -251,8 +251,9 @@ constexpr int kMaxSplits = 8;  // CTAs of a cluster that share the first contrac
 // parts cut off (not rounded, so none overflows) hold all 24 bits.  fp16 parts
 // are of the sum times a power of two that brings the largest finite one of
 // its block (64 ranks of a row, or all where there are fewer) to [2^14, 2^15):
-// two rounded parts leave at most 2^-24 of a sum, or 2^-40 of the block's
-// largest where that is more.
+// two rounded parts leave at most 2^-23 of a sum (half a step of the second, whose
+// size is at most 2^-11 of the first's binade), or 2^-39 of the block's largest
+// where that is more (half of fp16's smallest step, 2^-25, of 2^14).
 template <bool BF16>
 constexpr int kParts = BF16 ? 3 : 2;
 
