@@ -378,6 +378,7 @@ int seedlm_block_norm(const seedlm_norm* nm, int32_t M, const float* y, int64_t 
   if (nm->kind != SEEDLM_NORM_RMS && nm->kind != SEEDLM_NORM_LAYER) return SEEDLM_EINVAL;
   if (!any_dtype(nm->dtype) || (nm->post | 1) != 1 || (nm->pre | 1) != 1) return SEEDLM_EINVAL;
   if (!(nm->eps >= 0.f)) return SEEDLM_EINVAL;
+  if (M == 0 || nm->cols == 0) return SEEDLM_OK;  // empty arrays have no address
   if ((!y && !h) || (!h_out && !x)) return SEEDLM_EINVAL;
   if ((h || h_out) && !any_dtype(h_dtype)) return SEEDLM_EINVAL;
   if (x && !act_dtype(x_dtype)) return SEEDLM_EINVAL;
@@ -390,7 +391,6 @@ int seedlm_block_norm(const seedlm_norm* nm, int32_t M, const float* y, int64_t 
   if (h_out && (!aligned(h_out, hb) || ldho < nm->cols)) return SEEDLM_EINVAL;
   if (h && h == h_out && ldh != ldho) return SEEDLM_EINVAL;
   if (x && (!aligned(x, 2) || ldx < nm->cols)) return SEEDLM_EINVAL;
-  if (M == 0 || nm->cols == 0) return SEEDLM_OK;
   DeviceInfo dev;
   int rc = device_info(&dev);
   if (rc) return rc;
