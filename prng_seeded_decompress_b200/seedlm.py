@@ -282,7 +282,7 @@ def gemm_workspace(fmt, M: int, device=None):
     calls that share it must not run concurrently."""
     import torch
     n = gemm_workspace_bytes(fmt, M)
-    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 def gemm_smallM(fmt, rec, eplane, X, Y, workspace=None, stream=None):
@@ -531,7 +531,7 @@ class AdapterPlan:
         if words < 0:
             _check("seedlm_adapters_plan_words", words)
         self.M, self.n = int(M), int(n)
-        self.buffer = torch.zeros(words, dtype=torch.int32, device=device or "cuda")
+        self.buffer = torch.zeros(words, dtype=torch.int32, device="cuda" if device is None else device)
         self.order = self.buffer[:self.M]
         self.offsets = self.buffer[self.M:self.M + self.n + 1]
 

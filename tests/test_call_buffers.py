@@ -103,6 +103,20 @@ def test_a_products_workspace_is_made_on_the_calls_stream(sl, made_on, monkeypat
     assert made_on(calls) == [handle, handle]
 
 
+@pytest.mark.parametrize("device,want", [(None, "cuda"), (0, 0), (1, 1), ("cuda:0", "cuda:0")])
+def test_device_0_is_device_0(sl, monkeypatch, device, want):
+    seen, real = [], torch.zeros
+
+    def zeros(*size, dtype=None, device=None):
+        seen.append(device)
+        return real(*size, dtype=dtype)
+    monkeypatch.setattr(torch, "zeros", zeros)
+    monkeypatch.setattr(sl, "gemm_workspace_bytes", lambda f, M: 1000)
+    sl.AdapterPlan(4, 3, device=device)
+    sl.gemm_workspace(None, 4, device=device)
+    assert seen == [want, want]
+
+
 def batch(M, seed):
     g = torch.Generator().manual_seed(seed)
     whole = lambda *s: torch.randint(-2, 3, s, generator=g)  # noqa: E731
