@@ -269,9 +269,11 @@ SEEDLM_API uint32_t seedlm_lfsr_taps(int32_t K);
  * the pages: the method compresses the products' weights and leaves these as
  * they are).  They take and give the products' own types -- fp32 sums out of
  * a product, fp16 or bf16 activations into one -- and follow the conventions
- * above; leading dimensions and strides count elements.  Every kernel waits
- * for the work before it on the stream before it reads or writes memory, so
- * calls chain with the products without synchronisation.
+ * above; leading dimensions and strides count elements.  Every call reads and
+ * writes memory only after the work before it on the stream (the second kernel
+ * of seedlm_adapters_apply reads what the first does not write while that one
+ * runs, which has waited for the work before), so calls chain with the products
+ * without synchronisation.
  *
  * Low-rank adapters beside a shared projection.  The projection's outputs
  * are cut into `slices` parts (q, k, v of a fused projection; gate and up),
@@ -382,7 +384,7 @@ SEEDLM_API int seedlm_block_norm(const seedlm_norm* nm, int32_t M, const float* 
 /* The gated activation between a fused gate+up product and the down product:
  * X[m][f] = act(GU[m][f]) * GU[m][cols + f], GU M x 2 cols fp32, X M x cols
  * SEEDLM_F16 or SEEDLM_BF16, computed in fp32 and rounded once; cols at most
- * 2^30.
+ * 2^30.  X must not overlap GU.
  *   SILU: g / (1 + e^-g)   GELU: g/2 (1 + erf(g / sqrt 2))
  *   GELU_TANH: g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
 enum { SEEDLM_SILU = 0, SEEDLM_GELU = 1, SEEDLM_GELU_TANH = 2 };

@@ -65,7 +65,7 @@ __device__ __forceinline__ void cluster_sync() {
 // over the bins.  A second walk over the same rows puts each at its place.
 // Latency bound: a few dependent steps, so each lane has 16 of its rows' ids in
 // flight at once and keeps them for the second walk where they are all it has
-// (64 rows: 3.3 us, 16384 rows of 500 adapters: 10.6 us, 38 us with one CTA and
+// (64 rows: 3.3 us, 16384 rows of 500 adapters: 10.8 us, 38 us with one CTA and
 // the ids read again one by one).
 constexpr int kPlanThreads = 1024, kPlanCtas = 8;
 constexpr int kPlanSteps = 16;  // ids a lane holds
@@ -572,7 +572,10 @@ __device__ __forceinline__ void store_sums(const ApplyArgs& p, const float* sums
 // warp 32 columns of that at a time.  Each warp keeps a ring of its next steps
 // coming into shared memory; a lane copies exactly what it will itself read, so
 // the ring needs no barrier.  64 rows with adapters of their own, rank 64, two
-// slices of 8192 columns: 135 MB in 32 us (4.3 TB/s).
+// slices of 8192 columns: 135 MB in 31 us (4.4 TB/s).  Rows that are not aligned to
+// 16 bytes come raw, two words for each unit: their ring (123 kB for 32 slots, 184
+// for 64) leaves one CTA on an SM, and 333 rows of 4099 columns (392 CTAs, four or
+// five steps for a warp) take 20 us in three rounds.
 template <int RB>
 constexpr int kShrinkLowStages = RB == 4 ? 5 : 6;
 template <int RB, bool WIDE>
@@ -728,8 +731,9 @@ adapters_shrink_low_kernel(const __grid_constant__ ApplyArgs p) {
 // us, 57 with the same products on mma.sync.  The tensor
 // cores cut off what an addition leaves below a sum's last bit, so the stages go
 // to four sums in turn, which after every 32 stages are added up in fp32, rounded.
-// Rows that are not aligned to 16 bytes (not WIDE) come raw, nine words for 64
-// elements, and each thread shifts what it copied into place when it is there.
+// Rows that are not aligned to 16 bytes (not WIDE) come raw, two words for each
+// unit of 8 elements, and each thread shifts what it copied into place when it is
+// there.
 template <bool WIDE>
 struct ShrinkTallLayout {
   static constexpr int kThreads = 256, kStages = WIDE ? 4 : 2, kCols = 64, kSlots = 128, kSums = 4, kFlush = 32;
@@ -1175,7 +1179,7 @@ adapters_expand_low_kernel(const __grid_constant__ ApplyArgs p, int chunks, int 
 // with these.  B for the next 256 outputs arrives meanwhile: its one place is
 // free as soon as the products are done.  Each CTA goes through its share of all
 // (tile, slice, 256 outputs), in that order, fetching S once for a tile.  4096
-// rows, eight adapters of rank 64, 57344 outputs: 335 us for 1.94 GB (5.8 TB/s);
+// rows, eight adapters of rank 64, 57344 outputs: 338 us for 1.94 GB (5.7 TB/s);
 // the products of the same tiles on mma.sync, with the parts of S read from
 // shared memory by every warp, took 500.
 //
@@ -1515,8 +1519,14 @@ int slots_of(const seedlm_adapters& ad) { return ad.rank <= 32 ? 32 : (ad.rank +
 // outputs, 64 rows: low 48.9, tall 29.7.  Where X or A is not aligned to 16 bytes
 // a low tile costs more: 1.3 leaves at most 21 % at 180 places (1: 49 %; four
 // adapters, rank 20, 4099 inputs and outputs, 512 rows: 32.0 low, 25.2 tall).
-// The tiles are counted as if the rows were dealt evenly: how they are is on the
-// device.
+// The tiles are counted as if the rows were dealt evenly to all n adapters, and
+// the measurements deal them so: how they are is on the device.  It matters little
+// how uneven the rows of the adapters in use are (4096 rows, eight adapters, rank
+// 64, two slices of 28672 outputs: 365 us evenly, 355 with nine in ten rows on
+// one), much how many are in use at all: 2048 rows on four adapters there take
+// 190 us with n = 4, 213 with n = 64 and 445 with n = 1024; 512 rows on one, rank 16,
+// q, k, v of 4096 columns 17, 28 and 29.  A batch that uses few of many is better
+// served by a description of those alone.
 bool takes_low_tiles(const seedlm_adapters& ad, int M, bool wide) {
   const double low_cost = (1 + 0.03 * slots_of(ad)) * (wide ? 1 : 1.3);
   double size = (double)ad.slices * ad.cols;

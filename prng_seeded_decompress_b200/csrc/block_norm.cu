@@ -224,7 +224,10 @@ __device__ __forceinline__ void weigh(float (&v)[NV][4], const seedlm_norm& nm, 
 }
 
 // One CTA a row, which stays in registers: y and h are read once, h' and x
-// written once.  For few rows, where latency counts: a row of 8192, 3.2 us.
+// written once.  For few rows, where latency counts (a row of 8192, 3.3 us), and
+// for any number of rows of 8193 to 16384 (2048 of 16384, both norms, bf16: 85 us
+// for 336 MB; nothing of the next row is on its way).  Unaligned rows of that
+// width spill 236 bytes at 64 registers.
 constexpr int kRowThreads = 1024;
 
 template <int NV, bool VEC>
@@ -281,8 +284,9 @@ __global__ void __launch_bounds__(kRowThreads) block_norm_kernel(const __grid_co
 // A thread copies exactly what it will itself read, as soon as it has taken the
 // row before out of the same place, so the copies need no barrier.  256 threads
 // hold a row of 8192; the CTAs of an SM wait for their sums in turn.  4096 rows
-// of 8192, both norms, bf16: 62 us (5.4 TB/s), 85 with a CTA for each row; bound
-// by its instructions (2.4 issued a clock) and the two sums of a row.
+// of 8192, both norms, bf16: 63 us (5.3 TB/s), 85 with a CTA for each row; bound
+// by its instructions (2.4 issued a clock) and the two sums of a row.  Every form
+// spills, 24 to 72 bytes at 128 registers.
 constexpr int kStreamGroups = 8, kStreamThreads = 256, kStreamSums = 2 * 4 * 32 * 4;
 
 // Asynchronous copy of 8 or 16 bytes to shared memory.
@@ -686,7 +690,8 @@ __device__ __forceinline__ float activate(float g) {
 }
 
 // Bound by memory: 2048 x 14336 in 44 us (6.7 TB/s).  Narrow rows share a CTA: a
-// CTA costs more to start than they do (3168 rows of 200: 6.9 us, 18.1 with one each).
+// CTA costs more to start than they do (3168 rows of 200: 6.6 us, 18.1 with one each).
+// Unaligned rows go element by element: 4096 x 1001 takes 18 us for 41 MB.
 constexpr int kGluThreads = 256, kGluGroups = 2;  // groups of four outputs a thread
 
 template <int ACT, bool VEC, bool NARROW>
